@@ -47,6 +47,8 @@
  *   SWA KV           : per token 512 E4M3 bytes and one fp32 scale (value =
  *                      e4m3 * scale): the sliding-window KV stays FP8 ([Jdon]).
  *   bf16             : IEEE bfloat16 bit patterns (uint16).
+ *   paged rows       : the SWA KV row (512 E4M3 bytes, one fp32 scale) in pages of a
+ *                      pool, named by a page table (csa2_pages below).
  */
 #ifndef CSA2_C_ABI_H
 #define CSA2_C_ABI_H
@@ -307,7 +309,9 @@ typedef enum {
     CSA2_OP_POOL_BUILD = 1,
     CSA2_OP_POOL_TOPK = 2,
     CSA2_OP_SPARSE_ATTN = 3,
-    CSA2_OP_LAYER = 4
+    CSA2_OP_LAYER = 4,
+    CSA2_OP_WINDOW_ATTN = 5,   /* cap = most keys a query sees: min(window + n_sink, max_pages page_size); k, P unused */
+    CSA2_OP_PREFIX_ATTN = 6    /* cap = max_pages page_size of the prefix plus that of the own pages; k, P unused */
 } csa2_op;
 CSA2_API size_t csa2_workspace_bytes(csa2_op op, int32_t B, int32_t Q, int64_t cap, int32_t k, int32_t P);
 
@@ -419,6 +423,94 @@ CSA2_API csa2_status csa2_index_topk_noalloc(const uint8_t* q, const uint8_t* q_
  * flag is reset on `stream`.  Allocates nothing.
  */
 CSA2_API csa2_status csa2_index_topk_noalloc_status(int32_t clear, void* stream);
+
+/*
+ * Paged cache of FP8 latent rows (K = V = the row), for the layers that attend
+ * without a selection: the pure sliding-window layers ([Blog] "CSA2" section: the
+ * first encoder layers are pure SWA, FP8 KV) and dense attention behind a prefix
+ * that a batch shares (prefix caching).  The pages give no page layout; this is
+ * the plainest one, with the SWA KV's row format.
+ *   kv        device [n_pages][page_size][512]  E4M3 bytes, 16-byte aligned
+ *   kv_sc     device fp32 [n_pages][page_size]  token scales (value = e4m3 * scale), >= 0
+ *   table     device int32 [B][max_pages]  page of each page_size tokens of a sequence;
+ *             an id outside [0, n_pages) names no page: its tokens are not visible,
+ *             and new rows for it are dropped (a page given back is set to -1)
+ *   n_tokens  device int32 [B]  tokens stored (clamped to [0, max_pages page_size]);
+ *             token position p of sequence b is slot (p - pos0) % page_size of page
+ *             table[b][(p - pos0) / page_size], for pos0 <= p < pos0 + n_tokens[b]
+ *   page_size a multiple of 8, 8..4096;  n_pages page_size and pos0 + max_pages page_size below 2^31
+ *   pos0      token position of the tables' first slot (0, or the length of a shared prefix)
+ * Slots of no visible token may hold any bytes.  E4M3 NaN bytes and negative,
+ * infinite or NaN scales in a slot that a query of the call sees are not valid input.
+ */
+typedef struct csa2_pages {
+    uint8_t* kv;
+    float* kv_sc;
+    const int32_t* table;
+    const int32_t* n_tokens;
+    int64_t n_pages;
+    int32_t page_size, B, max_pages, pos0;
+} csa2_pages;
+
+/*
+ * Append to the paged cache: RMSNorm, RoPE by the token's own position, and the
+ * FP8 row, in one launch.  In fp32 for each row r with 0 <= seq[r] < B:
+ *   n = x / sqrt(mean(x^2) + eps) * norm_w   (n = x if normalise == 0)
+ *   for k = 0..31, (a, b) = (n_{448+2k}, n_{449+2k}):
+ *       a' = a cos t - b sin t,  b' = a sin t + b cos t,  t = pos[r] * inv_freq[k]
+ *       (the product in fp64, so that far positions keep their angle)
+ *   scale = amax|n| / 448;  code = E4M3 nearest (ties to even) to n / scale, 0 for a zero row
+ * and writes code and scale to the slot of position pos[r] of sequence seq[r].
+ *   x         device bf16, row r at x + r * x_stride elements; 16-byte aligned, x_stride a
+ *             multiple of 8, >= 512
+ *   seq, pos  device int32 [rows].  A row whose seq is outside [0, B), whose position is
+ *             outside the table or whose page id is out of range is dropped.  Rows
+ *             written by one call must name distinct slots.
+ *   inv_freq  device fp32 [32], or NULL for no rotation
+ *   norm_w    device fp32 [512], or NULL for weight 1
+ *   pages     host pointer (kv, kv_sc, table, sizes used; n_tokens is neither read nor
+ *             written: the caller counts its tokens)
+ */
+CSA2_API csa2_status csa2_pages_append(const void* x, int64_t x_stride, int64_t rows, const int32_t* seq,
+                                       const int32_t* pos, const float* inv_freq, const float* norm_w, float eps,
+                                       int32_t normalise, const csa2_pages* pages, void* stream);
+
+/*
+ * Sliding-window attention over the paged cache, with a few first tokens that
+ * stay visible: the query at token i of sequence b sees the stored tokens
+ *   { j <= i : j > i - window and j >= replay_start[b] }  and  { j <= i : j < n_sink },
+ * one softmax for each head: z_j = (q_h . k_j) * sm_scale, out_h = sum_j softmax(z)_j k_j.
+ *   q, out, lse   as for csa2_sparse_attn; a query that sees no token gets zeros and -inf
+ *   q_pos         device int32 [B][Q], any order, negative = no query (a shorter sequence)
+ *   window        >= 1 (2^31 - 1: causal attention over everything stored);  n_sink >= 0
+ *   replay_start  device int32 [B] or NULL
+ *   ws, ws_bytes  device workspace of csa2_workspace_bytes(CSA2_OP_WINDOW_ATTN, ...), 16-byte aligned;
+ *                 its contents do not matter.  Calls that may run at the same time need their own.
+ *   flag          device int32, zero before first use, or NULL: set to 1 when a device-side
+ *                 wait ran out of time (2 s); the results of that call are not valid.  Read
+ *                 it with csa2_flag_status.  Any number of calls can share it.
+ * Prefill chunks, replays and decode steps take the same call.
+ */
+CSA2_API csa2_status csa2_window_attn(const void* q, const csa2_pages* pages, const int32_t* q_pos, int32_t Q,
+                                      int32_t window, int32_t n_sink, const int32_t* replay_start, float sm_scale,
+                                      void* out, float* lse, void* ws, size_t ws_bytes, int32_t* flag, void* stream);
+
+/*
+ * Attention of a batch that shares a prefix: every query attends, under one
+ * causal softmax for each head, over the prefix (read once for all sequences) and its
+ * own sequence's tokens.  The query at token i of sequence b sees the tokens
+ * j <= i of `prefix` and of `pages` row b.
+ *   prefix  host pointer, prefix->B == 1
+ *   pages   host pointer: the sequences' own tokens, usually with pos0 = the prefix's length
+ *   q, q_pos, out, lse, ws, flag: as for csa2_window_attn (CSA2_OP_PREFIX_ATTN)
+ */
+CSA2_API csa2_status csa2_prefix_attn(const void* q, const csa2_pages* prefix, const csa2_pages* pages,
+                                      const int32_t* q_pos, int32_t Q, float sm_scale, void* out, float* lse, void* ws,
+                                      size_t ws_bytes, int32_t* flag, void* stream);
+
+/* Waits for `stream` and returns CSA2_ERR_TIMEOUT if the flag (device int32) is set, else
+ * CSA2_OK; with clear != 0 a set flag is reset to 0 on `stream`. */
+CSA2_API csa2_status csa2_flag_status(int32_t* flag, int32_t clear, void* stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,8 @@ TOPK, POOL_BLOCKS, WINDOW = 512, 2048, 128
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
-OP_INDEX_TOPK, OP_POOL_BUILD, OP_POOL_TOPK, OP_SPARSE_ATTN, OP_LAYER = range(5)
+(OP_INDEX_TOPK, OP_POOL_BUILD, OP_POOL_TOPK, OP_SPARSE_ATTN, OP_LAYER, OP_WINDOW_ATTN,
+ OP_PREFIX_ATTN) = range(7)
 MODE_FULL, MODE_REINDEX, MODE_REUSE = range(3)
 MODES = {"full": MODE_FULL, "reindex": MODE_REINDEX, "reuse": MODE_REUSE}
 
@@ -29,6 +30,12 @@ class csa2_kv(ctypes.Structure):
     _fields_ = [("lat", ctypes.c_void_p), ("lat_sc", ctypes.c_void_p), ("ik", ctypes.c_void_p),
                 ("ik_sc", ctypes.c_void_p), ("n_entries", ctypes.c_void_p), ("cap", ctypes.c_int64),
                 ("m", ctypes.c_int32)]
+
+
+class csa2_pages(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("kv_sc", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("pos0", ctypes.c_int32)]
 
 
 class csa2_layer_args(ctypes.Structure):
@@ -49,7 +56,7 @@ EXPORTS = ["csa2_status_str", "csa2_last_cuda_error", "csa2_quant_nvfp4", "csa2_
            "csa2_index_topk",
            "csa2_pool_build", "csa2_pool_topk", "csa2_sparse_attn", "csa2_workspace_bytes", "csa2_layer_step",
            "csa2_index_topk_noalloc", "csa2_index_topk_noalloc_status", "csa2_device_status", "csa2_front_end",
-           "csa2_test_starve_copies"]
+           "csa2_test_starve_copies", "csa2_pages_append", "csa2_window_attn", "csa2_prefix_attn", "csa2_flag_status"]
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -62,7 +69,7 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sparse_attention_fp4_quant_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    KVP = ctypes.POINTER(csa2_kv)
+    KVP, PGP, f32 = ctypes.POINTER(csa2_kv), ctypes.POINTER(csa2_pages), ctypes.c_float
     sig = {
         "csa2_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "csa2_last_cuda_error": (ctypes.c_int, []),
@@ -81,6 +88,10 @@ def lib():
         "csa2_index_topk_noalloc_status": (ctypes.c_int, [i32, P]),
         "csa2_test_starve_copies": (None, [i32]),
         "csa2_front_end": (ctypes.c_int, [P, i64, P, P, P, ctypes.c_float, P, P, P, P, P, P, i64, P, P]),
+        "csa2_pages_append": (ctypes.c_int, [P, i64, i64, P, P, P, P, f32, i32, PGP, P]),
+        "csa2_window_attn": (ctypes.c_int, [P, PGP, P, i32, i32, i32, P, f32, P, P, P, sz, P, P]),
+        "csa2_prefix_attn": (ctypes.c_int, [P, PGP, PGP, P, i32, f32, P, P, P, sz, P, P]),
+        "csa2_flag_status": (ctypes.c_int, [P, i32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -441,3 +452,159 @@ def csa2_layer_step(mode, kv, q_pos, q, swa, swa_sc, swa_pos0, idx, k=TOPK, iq=N
     a.ws_bytes = ws.numel()
     _check(lib().csa2_layer_step(ctypes.byref(a), _stream()))
     return out
+
+
+# ---- the paged FP8 cache -----------------------------------------------------------------------
+
+def _on(t, dtype, numel, name, dev):
+    """A contiguous tensor of this dtype and size on the current device (number dev)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {dtype} on cuda:{dev}, the current device, got "
+                         f"{t.dtype} on {t.device} with strides {t.stride()}")
+    if t.numel() != numel:
+        raise ValueError(f"{name}: expected {numel} elements, got {t.numel()} (shape {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+class Pages:
+    """A paged cache of FP8 latent rows (device tensors) and its csa2_pages view.
+
+    kv u8 [n_pages, page_size, 512], kv_sc f32 [n_pages, page_size], table i32 [B, max_pages] (-1 = no
+    page), n_tokens i32 [B] (both written by the caller, in place); pos0 is the token position of the
+    tables' first slot.  Several Pages can share one pool: a shared prefix has a table of its own."""
+
+    def __init__(self, B, max_pages, n_pages=None, page_size=64, pos0=0, device="cuda"):
+        n_pages = B * max_pages if n_pages is None else n_pages
+        self._set(torch.zeros((n_pages, page_size, D), dtype=torch.uint8, device=device),
+                  torch.zeros((n_pages, page_size), dtype=torch.float32, device=device),
+                  torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                  torch.zeros((B,), dtype=torch.int32, device=device), pos0)
+
+    @classmethod
+    def of(cls, kv, kv_sc, table, n_tokens, pos0=0):
+        """The cache over tensors that the caller holds."""
+        self = cls.__new__(cls)
+        self._set(kv, kv_sc, table, n_tokens, pos0)
+        return self
+
+    def _set(self, kv, kv_sc, table, n_tokens, pos0):
+        if kv.dim() != 3 or kv.shape[2] != D or table.dim() != 2:
+            raise ValueError(f"expected kv [n_pages, page_size, {D}] and table [B, max_pages], got "
+                             f"{tuple(kv.shape)} and {tuple(table.shape)}")
+        (n_pages, ps, _), (B, width) = kv.shape, table.shape
+        if n_pages < 1 or B < 1 or width < 1 or ps < 8 or ps > 4096 or ps % 8:
+            raise ValueError(f"page_size must be a multiple of 8 in 8..4096 and all sizes positive, got {n_pages} pages "
+                             f"of {ps} tokens, table {B} x {width}")
+        if pos0 < 0 or pos0 + width * ps >= 2 ** 31 or n_pages * ps >= 2 ** 31:
+            raise ValueError("positions and pool rows must be below 2^31")
+        self.device = kv.get_device()
+        for t, dt, n, name in ((kv, torch.uint8, n_pages * ps * D, "kv"), (kv_sc, torch.float32, n_pages * ps, "kv_sc"),
+                               (table, torch.int32, B * width, "table"), (n_tokens, torch.int32, B, "n_tokens")):
+            _on(t, dt, n, name, self.device)
+        self._t = (kv, kv_sc, table, n_tokens)
+        self.n_pages, self.page_size, self.B, self.max_pages, self.pos0 = n_pages, ps, B, width, pos0
+        self._c = csa2_pages(kv.data_ptr(), kv_sc.data_ptr(), table.data_ptr(), n_tokens.data_ptr(), n_pages, ps, B,
+                             width, pos0)
+
+    kv = property(lambda self: self._t[0])
+    kv_sc = property(lambda self: self._t[1])
+    table = property(lambda self: self._t[2])
+    n_tokens = property(lambda self: self._t[3])
+
+    @property
+    def cap(self):
+        """Tokens that the table can name for a sequence."""
+        return self.max_pages * self.page_size
+
+    def c(self, dev):
+        if self.device != dev:
+            raise ValueError(f"the pages are on cuda:{self.device}, the current device is cuda:{dev}")
+        return self._c
+
+
+_flags = {}
+
+
+def _flag(dev):
+    """This device's sticky error flag of the paged attentions (kept for the life of the process, so
+    that captured graphs can name it)."""
+    if dev not in _flags:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("make one paged attention call on this device before capturing one into a graph")
+        _flags[dev] = torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+        torch.cuda.current_stream().synchronize()   # other streams may use it next
+    return _flags[dev]
+
+
+def csa2_flag_status(clear=False):
+    """Waits for the current stream; raises CSA2Error (CSA2_ERR_TIMEOUT) if a paged attention call on
+    the current device had a device-side wait run out of time (its results are not valid)."""
+    _check(lib().csa2_flag_status(_ptr(_flag(torch.cuda.current_device())), 1 if clear else 0, _stream()))
+
+
+def csa2_pages_append(x, pages, seq, pos, inv_freq=None, norm_w=None, eps=1e-6, normalise=True):
+    """x bf16 [rows, 512] (rows may be strided) -> RMSNorm, RoPE at pos, FP8 rows in the slots of
+    (seq i32 [rows], pos i32 [rows]); rows with seq < 0 or no page are dropped.  inv_freq f32 [32],
+    norm_w f32 [512] or None.  The caller updates pages.n_tokens."""
+    dev = torch.cuda.current_device()
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev or x.dim() != 2 or x.shape[1] != D or x.stride(1) != 1:
+        raise ValueError(f"x: expected bf16 rows [rows, {D}] on cuda:{dev}, got {x.dtype} {tuple(x.shape)} on {x.device} "
+                         f"with strides {x.stride()}")
+    rows = x.shape[0]
+    stride = x.stride(0) if rows > 1 else D
+    _check(lib().csa2_pages_append(
+        x.data_ptr(), stride, rows, _on(seq, torch.int32, rows, "seq", dev), _on(pos, torch.int32, rows, "pos", dev),
+        None if inv_freq is None else _on(inv_freq, torch.float32, 32, "inv_freq", dev),
+        None if norm_w is None else _on(norm_w, torch.float32, D, "norm_w", dev), eps, 1 if normalise else 0,
+        pages.c(dev), torch.cuda.current_stream().cuda_stream))
+
+
+def _pages_attn_outputs(q, q_pos, pages, out, lse, dev):
+    if q_pos.dim() != 2 or q_pos.shape[0] != pages.B:
+        raise ValueError(f"q_pos: expected [{pages.B}, Q], got {tuple(q_pos.shape)}")
+    n = q_pos.numel()
+    if out is None:
+        out = torch.empty((*q_pos.shape, H, D), dtype=torch.bfloat16, device=q.device)
+    if lse is True:
+        lse = torch.empty((*q_pos.shape, H), dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    return (out, lse, _on(q, torch.bfloat16, n * H * D, "q", dev), _on(q_pos, torch.int32, n, "q_pos", dev),
+            _on(out, torch.bfloat16, n * H * D, "out", dev),
+            None if lse is None else _on(lse, torch.float32, n * H, "lse", dev))
+
+
+def _scratch(op, pages, Q, keys, ws, device):
+    """A workspace of this call's own (torch's allocator orders its reuse by stream, and a captured call
+    keeps its in the graph's pool), or the caller's."""
+    if ws is None:
+        ws = torch.empty(lib().csa2_workspace_bytes(op, pages.B, Q, keys, 0, 0), dtype=torch.uint8, device=device)
+    return ws
+
+
+def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None, sm_scale=1.0 / math.sqrt(D),
+                     out=None, lse=False, ws=None):
+    """Sliding-window attention over a paged cache; tokens at positions below n_sink stay visible.
+    q bf16 [B,Q,16,512], q_pos i32 [B,Q] (negative = no query) -> out bf16 [B,Q,16,512] (, lse f32 [B,Q,16])."""
+    dev = torch.cuda.current_device()
+    pg = pages.c(dev)
+    out, lse, qp, pp, op, lp = _pages_attn_outputs(q, q_pos, pages, out, lse, dev)
+    rp = None if replay_start is None else _on(replay_start, torch.int32, pages.B, "replay_start", dev)
+    Q = q_pos.shape[1]
+    ws = _scratch(OP_WINDOW_ATTN, pages, Q, min(window + n_sink, pages.cap), ws, q.device)
+    _check(lib().csa2_window_attn(qp, pg, pp, Q, window, n_sink, rp, sm_scale, op, lp, ws.data_ptr(),
+                                  ws.numel(), _flag(dev).data_ptr(), torch.cuda.current_stream().cuda_stream))
+    return out if lse is None else (out, lse)
+
+
+def csa2_prefix_attn(q, prefix, pages, q_pos, sm_scale=1.0 / math.sqrt(D), out=None, lse=False, ws=None):
+    """Attention of a batch over a shared prefix (Pages of one table row) and each sequence's own pages,
+    under one causal softmax.  q bf16 [B,Q,16,512], q_pos i32 [B,Q] -> out bf16 (, lse f32 [B,Q,16])."""
+    dev = torch.cuda.current_device()
+    pf, pg = prefix.c(dev), pages.c(dev)
+    out, lse, qp, pp, op, lp = _pages_attn_outputs(q, q_pos, pages, out, lse, dev)
+    Q = q_pos.shape[1]
+    ws = _scratch(OP_PREFIX_ATTN, pages, Q, prefix.cap + pages.cap, ws, q.device)
+    _check(lib().csa2_prefix_attn(qp, pf, pg, pp, Q, sm_scale, op, lp, ws.data_ptr(), ws.numel(),
+                                  _flag(dev).data_ptr(), torch.cuda.current_stream().cuda_stream))
+    return out if lse is None else (out, lse)

@@ -49,6 +49,25 @@ SelectParams select_params(const csa2_kv* kv, const int32_t* q_pos, int B, int Q
     return p;
 }
 
+bool pages_ok(const csa2_pages* p) {
+    if (!p || !p->kv || !p->kv_sc || !p->table || !p->n_tokens || !aligned16(p->kv)) return false;
+    if (p->page_size < 8 || p->page_size > 4096 || p->page_size % 8 != 0) return false;
+    const int64_t lim = int64_t(1) << 31;
+    if (p->B < 1 || p->max_pages < 1 || p->pos0 < 0 || p->n_pages < 1) return false;
+    return p->n_pages < lim / p->page_size && (int64_t)p->max_pages * p->page_size + p->pos0 < lim;
+}
+
+// Arguments shared by the two attentions over the paged cache.
+bool pages_attn_ok(const void* q, const csa2_pages* pages, const int32_t* q_pos, int32_t Q, float sm_scale,
+                   const void* out, const void* ws) {
+    if (!pages_ok(pages) || !q || !q_pos || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
+        return false;
+    if (!(sm_scale > 0.0f) || !(sm_scale < 1e30f)) return false;
+    return Q >= 1 && (int64_t)pages->B * Q <= 65535;
+}
+
+int64_t pages_cap(const csa2_pages* p) { return (int64_t)p->max_pages * p->page_size; }
+
 }  // namespace
 
 namespace csa2 {
@@ -139,6 +158,8 @@ size_t csa2_workspace_bytes(csa2_op op, int32_t B, int32_t Q, int64_t cap, int32
             if (d > m) m = d;
             return m;
         }
+        case CSA2_OP_WINDOW_ATTN: return pages_attn_ws_bytes(false, B, Q, cap);
+        case CSA2_OP_PREFIX_ATTN: return pages_attn_ws_bytes(true, B, Q, cap);
     }
     return 0;
 }
@@ -309,6 +330,73 @@ csa2_status csa2_layer_step(const csa2_layer_args* a, void* stream) {
     return csa2_sparse_attn(a->q, kv, a->idx, a->k, a->swa, a->swa_sc, a->swa_pos0, a->T, a->window,
                             a->replay_start, a->q_pos, a->B, a->Q, a->sm_scale, a->out, a->lse, a->ws, a->ws_bytes,
                             stream);
+}
+
+csa2_status csa2_pages_append(const void* x, int64_t x_stride, int64_t rows, const int32_t* seq, const int32_t* pos,
+                              const float* inv_freq, const float* norm_w, float eps, int32_t normalise,
+                              const csa2_pages* pages, void* stream) {
+    if (rows < 0 || rows > (int64_t(1) << 31) - 1 || !pages_ok(pages)) return CSA2_ERR_INVALID_ARG;
+    if (rows == 0) return CSA2_OK;
+    if (!x || !seq || !pos || !aligned16(x) || x_stride < CSA2_D || x_stride % 8 != 0) return CSA2_ERR_INVALID_ARG;
+    if (normalise && !(eps >= 0.0f)) return CSA2_ERR_INVALID_ARG;
+    if (norm_w && !aligned16(norm_w)) return CSA2_ERR_INVALID_ARG;
+    return cuda_status(launch_pages_append(x, x_stride, rows, seq, pos, inv_freq, norm_w, eps, normalise != 0, *pages,
+                                           (cudaStream_t)stream));
+}
+
+csa2_status csa2_window_attn(const void* q, const csa2_pages* pages, const int32_t* q_pos, int32_t Q, int32_t window,
+                             int32_t n_sink, const int32_t* replay_start, float sm_scale, void* out, float* lse,
+                             void* ws, size_t ws_bytes, int32_t* flag, void* stream) {
+    if (!pages_attn_ok(q, pages, q_pos, Q, sm_scale, out, ws) || window < 1 || n_sink < 0) return CSA2_ERR_INVALID_ARG;
+    int64_t keys = (int64_t)window + n_sink;
+    if (keys > pages_cap(pages)) keys = pages_cap(pages);
+    if (ws_bytes < pages_attn_ws_bytes(false, pages->B, Q, keys)) return CSA2_ERR_WORKSPACE;
+    PagesAttnParams p{};
+    p.q = (const uint16_t*)q;
+    p.own = *pages;
+    p.q_pos = q_pos;
+    p.B = pages->B;
+    p.Q = Q;
+    p.window = window;
+    p.n_sink = n_sink;
+    p.replay_start = replay_start;
+    p.sm_scale = sm_scale;
+    p.out = (uint16_t*)out;
+    p.lse = lse;
+    p.flag = flag;
+    return cuda_status(launch_pages_attn(p, keys, ws, (cudaStream_t)stream));
+}
+
+csa2_status csa2_prefix_attn(const void* q, const csa2_pages* prefix, const csa2_pages* pages, const int32_t* q_pos,
+                             int32_t Q, float sm_scale, void* out, float* lse, void* ws, size_t ws_bytes, int32_t* flag,
+                             void* stream) {
+    if (!pages_attn_ok(q, pages, q_pos, Q, sm_scale, out, ws) || !pages_ok(prefix) || prefix->B != 1)
+        return CSA2_ERR_INVALID_ARG;
+    const int64_t keys = pages_cap(prefix) + pages_cap(pages);
+    if (ws_bytes < pages_attn_ws_bytes(true, pages->B, Q, keys)) return CSA2_ERR_WORKSPACE;
+    PagesAttnParams p{};
+    p.q = (const uint16_t*)q;
+    p.prefix = *prefix;
+    p.own = *pages;
+    p.q_pos = q_pos;
+    p.B = pages->B;
+    p.Q = Q;
+    p.window = 0x7FFFFFFF;
+    p.sm_scale = sm_scale;
+    p.out = (uint16_t*)out;
+    p.lse = lse;
+    p.flag = flag;
+    return cuda_status(launch_pages_attn(p, keys, ws, (cudaStream_t)stream));
+}
+
+csa2_status csa2_flag_status(int32_t* flag, int32_t clear, void* stream) {
+    if (!flag) return CSA2_ERR_INVALID_ARG;
+    int32_t v = 0;
+    cudaError_t e = cudaMemcpyAsync(&v, flag, sizeof(v), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+    if (e == cudaSuccess && v && clear) e = cudaMemsetAsync(flag, 0, sizeof(v), (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_status(e);
+    return v ? CSA2_ERR_TIMEOUT : CSA2_OK;
 }
 
 }  // extern "C"

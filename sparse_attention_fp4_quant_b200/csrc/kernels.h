@@ -154,4 +154,27 @@ cudaError_t launch_attn(AttnParams& p, int S, cudaStream_t st);
 int attn_cluster_size(int B, int Q, int k, int window, int* main_per_cta, int* swa_per_cta);
 cudaError_t launch_attn_cluster(AttnParams& p, int C, cudaStream_t st);
 
+// Paged cache (pages.cu): append of new rows.
+cudaError_t launch_pages_append(const void* x, int64_t x_stride, int64_t rows, const int32_t* seq, const int32_t* pos,
+                                const float* inv_freq, const float* norm_w, float eps, bool normalise,
+                                const csa2_pages& pages, cudaStream_t st);
+
+// Attention over the paged cache (pages_attn.cu): the sliding-window form (prefix.B == 0)
+// and the shared-prefix form.
+struct PagesAttnParams {
+    const uint16_t* q;            // bf16 [B Q][16][512]
+    csa2_pages prefix;            // prefix.B == 0: none
+    csa2_pages own;
+    const int32_t* q_pos;         // [B Q]
+    int B, Q;
+    int window, n_sink;
+    const int32_t* replay_start;  // [B] or null
+    float sm_scale;
+    uint16_t* out;
+    float* lse;                   // or null
+    int32_t* flag;                // or null
+};
+size_t pages_attn_ws_bytes(bool prefix, int B, int Q, int64_t keys);
+cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, cudaStream_t st);
+
 }  // namespace csa2
