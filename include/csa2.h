@@ -98,8 +98,9 @@ CSA2_API int csa2_last_cuda_error(void);
  * with fewer than 8 per batch row) announce their first copy stage on its
  * barrier but issue no copy, so the CTAs' bounded waits (2 s) run out: the call
  * sets its sticky error flag (read by csa2_device_status or
- * csa2_index_topk_noalloc_status) and its results are not valid.  Nothing
- * faults or hangs; the context stays usable.
+ * csa2_index_topk_noalloc_status) and its results are not valid.  The attentions over
+ * the paged cache do the same (csa2_window_attn, csa2_prefix_attn; csa2_flag_status).
+ * Nothing faults or hangs; the context stays usable.
  */
 CSA2_API void csa2_test_starve_copies(int32_t enable);
 
