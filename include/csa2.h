@@ -432,7 +432,7 @@ CSA2_API csa2_status csa2_index_topk_noalloc_status(int32_t clear, void* stream)
  * that a batch shares (prefix caching).  The pages give no page layout; this is
  * the plainest one, with the SWA KV's row format.
  *   kv        device [n_pages][page_size][512]  E4M3 bytes, 16-byte aligned
- *   kv_sc     device fp32 [n_pages][page_size]  token scales (value = e4m3 * scale), >= 0
+ *   kv_sc     device fp32 [n_pages][page_size]  token scales (value = e4m3 * scale), >= 0, 16-byte aligned
  *   table     device int32 [B][max_pages]  page of each page_size tokens of a sequence;
  *             an id outside [0, n_pages) names no page: its tokens are not visible,
  *             and new rows for it are dropped (a page given back is set to -1)

@@ -50,7 +50,7 @@ SelectParams select_params(const csa2_kv* kv, const int32_t* q_pos, int B, int Q
 }
 
 bool pages_ok(const csa2_pages* p) {
-    if (!p || !p->kv || !p->kv_sc || !p->table || !p->n_tokens || !aligned16(p->kv)) return false;
+    if (!p || !p->kv || !p->kv_sc || !p->table || !p->n_tokens || !aligned16(p->kv) || !aligned16(p->kv_sc)) return false;
     if (p->page_size < 8 || p->page_size > 4096 || p->page_size % 8 != 0) return false;
     const int64_t lim = int64_t(1) << 31;
     if (p->B < 1 || p->max_pages < 1 || p->pos0 < 0 || p->n_pages < 1) return false;

@@ -32,51 +32,89 @@ namespace {
 using namespace tc;
 
 constexpr int kTileKeys = 128;
-constexpr int kGroup = 8;                              // keys per TMA box: rows of one swizzle atom
-constexpr int kTileGroups = kTileKeys / kGroup;
-constexpr int kTileBytes = kTileKeys * kD;             // 64 KB
-constexpr int kSoftmaxThreads = 128;
-constexpr int kThreads = kSoftmaxThreads + 64;         // + producer warp + MMA warp
+constexpr int kGroup = 8;                              // keys of one swizzle atom
+constexpr int kBlocks = kD / 128;                      // channel blocks: 128 channels of the tile's keys, 16 KB
+constexpr int kBlockBytes = kTileKeys * 128;
+constexpr int kWg = 128;                               // threads of a softmax warpgroup: one query, a thread per key
 constexpr float kHeadroom = 3.0f;                      // log2 of how far a weight may exceed the reference
 constexpr float kPScale = 4096.0f;                     // weight 1 at 2^12, 2^15 with the headroom: below f16's and E5M2's largest
 constexpr float kMinLogScale = -100.0f;                // token scales below 2^-100 count as 2^-100 in the reference
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-// One list of keys of a CTA: groups of 8 slots of one table row, `sink` first groups and then the
-// window's (virtual group v is group v, or v + delta from `sink` on), for queries [qa, qa + nq).
+// One list of keys of a CTA, for its queries [qa, qa + nq): units of `unit` slots of one table row (a unit is
+// one TMA box, inside one page), `sink` first units and then the window's (virtual unit v is unit v, or
+// v + delta from `sink` on).
 struct Seg {
     int tile0;      // first tile of the list in the CTA's order
-    int groups, sink, delta;
-    int which, b;   // 0 = prefix, 1 = own; table row
+    int units, sink, delta;
+    int own;        // 0 = the shared prefix, 1 = a sequence's own pages
     int qa, nq;
-    int end;        // first position behind the stored tokens
+    int pos0, end;  // position of slot 0, and of the first slot behind the stored tokens
+    int page_size, n_pages;
+    const int32_t* table;   // the sequence's row
+    const float* scales;
+
+    __device__ __forceinline__ int unit(int v) const { return v < sink ? v : v + delta; }
 };
+
+__device__ __forceinline__ Seg make_seg(const csa2_pages& pg, int own, int b, int tile0, int units, int sink, int delta,
+                                        int qa, int nq, int end) {
+    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, pg.page_size, (int)pg.n_pages,
+            pg.table + (int64_t)b * pg.max_pages, pg.kv_sc};
+}
 
 template <int NQ, int ST>
 struct Smem {
     static constexpr int R = kH * NQ;
-    alignas(1024) uint8_t K[ST][kTileBytes];     // [16 groups][4 channel blocks][8 keys][128 B], 128-byte swizzle
-    alignas(1024) uint8_t Qs[4][2 * R][128];     // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
-    alignas(1024) uint8_t P[3 * NQ][kTileKeys][16];   // [term][query]: 16 rows of each key, no swizzle
-    float wmax[4][R];
+    alignas(1024) uint8_t K[ST][kBlocks][kBlockBytes];   // [channel block][key][128 B], 128-byte swizzle
+    alignas(1024) uint8_t Qs[kBlocks][2 * R][128];       // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
+    alignas(1024) uint8_t P[3 * NQ][kTileKeys][16];      // [term][query]: 16 rows of each key, no swizzle
+    alignas(16) float sc[ST][kTileKeys];                 // the keys' token scales
+    uint8_t held[ST][kTileKeys / kGroup];                // whether a unit's page exists
+    alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
     alignas(16) float fac[R];
     alignas(16) float rowf[R];
-    float lsum[R];
     Seg seg[NQ + 1];
     int nseg, ntiles;
     int qi[NQ], qlow[NQ];
-    int rescale[2];
     int dead;
     uint32_t tmem;
-    uint64_t full[ST], empty[ST], s_full[2], p_full, pv_done, wind_down;
+    uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], p_full, pv_done, wind_down;
 };
 
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The issuing warp runs its loop converged and one elected lane (lead != 0) issues: descriptors then stay in
+// uniform registers.  Issued from a divergent branch, each MMA cost about 110 cycles of descriptor moves.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+
+// Phase test that returns at once.  The issuer watches two barriers: a try_wait on one may sleep past the other.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
         : "memory");
 }
 
@@ -88,11 +126,12 @@ __device__ __forceinline__ uint32_t idesc_pv(int N) {
 }
 constexpr uint32_t kSw128 = 2;
 
-__device__ __forceinline__ void tma_group(void* dst, const CUtensorMap* map, int group, uint64_t* bar) {
+// 128 channels (block c) of one unit's rows.
+__device__ __forceinline__ void tma_unit(void* dst, const CUtensorMap* map, int row, int c, uint64_t* bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
-        "[%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(0), "r"(group), "r"(smem_u32(bar))
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(0), "r"(row), "r"(c), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -116,7 +155,17 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
+// Barrier of one softmax warpgroup, alone or with the OR of a condition over its threads.
+__device__ __forceinline__ void wg_bar(int wg) { asm volatile("bar.sync %0, %1;" ::"r"(1 + wg), "n"(kWg) : "memory"); }
+__device__ __forceinline__ bool wg_any(int wg, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(1 + wg), "n"(kWg)
+        : "memory");
+    return r != 0;
+}
 
 // Two weights (f16x2) -> three terms of E5M2 in the high bytes of each half.  An E5M2 value is an
 // f16 whose low byte is zero: hi and mid truncate (each leaves a remainder of the next bits,
@@ -139,6 +188,7 @@ __device__ __forceinline__ int stored_end(const csa2_pages& pg, int b) {
 
 struct KernelArgs {
     PagesAttnParams p;
+    int unit;         // keys of a TMA box: 8 .. 128, divides every page
     int splits;
     int test_starve;  // test hook (csa2_test_starve_copies): the producer issues no copies
     float* part_o;    // [block][split][R][512]
@@ -146,7 +196,7 @@ struct KernelArgs {
 };
 
 template <int NQ, int ST>
-__global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
+__global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
     pages_attn_kernel(const __grid_constant__ CUtensorMap map_own, const __grid_constant__ CUtensorMap map_prefix,
                       const __grid_constant__ KernelArgs args) {
     using Sm = Smem<NQ, ST>;
@@ -159,26 +209,28 @@ __global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
     extern __shared__ uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const PagesAttnParams& p = args.p;
+    constexpr int kProducer = 4 * NQ, kIssuer = kProducer + 1;   // warps behind the softmax warpgroups
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int unit = args.unit, upt = kTileKeys / unit;   // keys of a unit, units of a tile
 
-    if (warp == 5) tmem_alloc(&sm.tmem, kTmemCols);
-    if (tid == kSoftmaxThreads) {
-        for (int s = 0; s < ST; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 1);
-        }
+    if (warp == kIssuer) tmem_alloc(&sm.tmem, kTmemCols);
+    if (tid == 32 * kProducer) {
+        for (int s = 0; s < ST; ++s)
+            for (int c = 0; c < kBlocks; ++c) {
+                mbar_init(&sm.full[s][c], 1);
+                mbar_init(&sm.empty[s][c], 1);
+            }
         mbar_init(&sm.s_full[0], 1);
         mbar_init(&sm.s_full[1], 1);
-        mbar_init(&sm.p_full, kSoftmaxThreads);
+        mbar_init(&sm.p_full, kWg * NQ);
         mbar_init(&sm.pv_done, 1);
         mbar_init(&sm.wind_down, 1);
         fence_mbar_init();
         sm.dead = 0;
-        sm.rescale[0] = sm.rescale[1] = 0;
     }
     pdl_enter();
 
-    // ---- this CTA's queries and key lists ----
+    // ---- this CTA's queries ----
     const bool shared_prefix = p.prefix.B != 0;
     int f0, nq;   // first query (b Q + q) and count
     if (shared_prefix) {
@@ -189,11 +241,62 @@ __global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
         f0 = b * p.Q + q0;
         nq = min(NQ, p.Q - q0);
     }
-    if (warp == 4) {
-        // lanes 0 .. NQ-1: a query each; its sequence's stored end; then lane 0 builds the lists
-        int i = -1, low = 0, end = 0;
+
+    // A bounded wait; the first to run out of time tells every other.
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t start = globaltimer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_wait(bar, parity)) return true;
+            if ((it & 63u) == 0u) {
+                if (*(volatile int*)&sm.dead) return false;
+                if (globaltimer_ns() - start > kTimeoutNs) {
+                    *(volatile int*)&sm.dead = 1;
+                    if (p.flag) *p.flag = 1;
+                    return false;
+                }
+            }
+        }
+    };
+    auto seg_of = [&](int tile) -> int {
+        int s = 0;
+        while (s + 1 < sm.nseg && tile >= sm.seg[s + 1].tile0) ++s;
+        return s;
+    };
+    auto first_tile = [&](int ntiles, int split) { return (int)((int64_t)ntiles * split / args.splits); };
+    // Producer: the copies of tile t, the CTA's n-th, channel block by channel block (one lane per unit).
+    auto load_tile = [&](int t, int n) -> bool {
+        const int st = n % ST;
+        const Seg& sg = sm.seg[seg_of(t)];
+        const int v = (t - sg.tile0) * upt + lane;
+        int row = -1;
+        if (lane < upt && v < sg.units) {
+            const int slot = sg.unit(v) * unit, pg = slot / sg.page_size, page = __ldg(sg.table + pg);
+            if (page >= 0 && page < sg.n_pages) row = page * sg.page_size + (slot - pg * sg.page_size);
+        }
+        const uint32_t live = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+        const CUtensorMap* map = sg.own ? &map_own : &map_prefix;
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c) {
+            bool ok = true;
+            if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
+            if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+            if (c == 0 && lane < upt) sm.held[st][lane] = row >= 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], live * unit * (c == 0 ? 128 + 4 : 128));
+            __syncwarp();
+            if (row >= 0 && !args.test_starve) {
+                tma_unit(sm.K[st][c] + lane * unit * 128, map, row, c, &sm.full[st][c]);
+                if (c == 0) bulk_load(&sm.sc[st][lane * unit], sg.scales + row, unit * 4, &sm.full[st][0]);
+            }
+        }
+        return true;
+    };
+
+    if (warp == kProducer) {
+        // lanes 0 .. NQ-1: a query each; then lane 0 writes the lists
+        int i = -1, low = 0, end = 0, pend = 0;
         const int b = (f0 + min(lane, nq - 1)) / p.Q;
-        int pend = 0;
         if (lane < nq) i = p.q_pos[f0 + lane];
         if (lane < NQ) end = stored_end(p.own, b);
         if (shared_prefix && lane == 0) pend = stored_end(p.prefix, 0);
@@ -208,16 +311,18 @@ __global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
         int n = 0, tiles = 0, imax = -1;
 #pragma unroll
         for (int c = 0; c < NQ; ++c) imax = max(imax, __shfl_sync(0xFFFFFFFFu, i, c));
-        if (shared_prefix && lane == 0) {
+        if (shared_prefix) {
+            pend = __shfl_sync(0xFFFFFFFFu, pend, 0);
             const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
             if (e > 0) {
-                const int g = (e + kGroup - 1) / kGroup;
-                sm.seg[n++] = {0, g, 0, 0, 0, 0, 0, nq, pend};
-                tiles = (g + kTileGroups - 1) / kTileGroups;
+                const int u = (e + unit - 1) / unit;
+                if (lane == 0) sm.seg[n] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend);
+                ++n;
+                tiles = (u + upt - 1) / upt;
             }
         }
         int qa = 0;
-        while (qa < nq) {   // runs of queries of one sequence (uniform over the warp)
+        while (qa < nq) {   // runs of queries of one sequence
             const int rb = __shfl_sync(0xFFFFFFFFu, b, qa), rend = __shfl_sync(0xFFFFFFFFu, end, qa);
             int c = qa, hi = 0, lo = 0x7FFFFFFF;
             while (c < nq && __shfl_sync(0xFFFFFFFFu, b, c) == rb) {
@@ -228,17 +333,18 @@ __global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
                 }
                 ++c;
             }
-            if (lane == 0 && hi > p.own.pos0) {
-                // sink groups, then the window's groups from the first that is not a sink group
-                const int base = p.own.pos0;
+            const int base = p.own.pos0;
+            if (hi > base) {
+                // the sinks' units, then the window's from the first that holds no sink
                 const int ns = min(p.n_sink, hi) - base;
-                const int gs = ns > 0 ? (ns + kGroup - 1) / kGroup : 0;
-                const int ge = (hi - base + kGroup - 1) / kGroup;
-                const int gw = max(gs, lo > base ? (lo - base) / kGroup : 0);
-                const int g = gs + max(0, ge - gw);
-                if (g > 0) {
-                    sm.seg[n++] = {tiles, g, gs, gw - gs, 1, rb, qa, c - qa, rend};
-                    tiles += (g + kTileGroups - 1) / kTileGroups;
+                const int us = ns > 0 ? (ns + unit - 1) / unit : 0;
+                const int ue = (hi - base + unit - 1) / unit;
+                const int uw = max(us, lo > base ? (lo - base) / unit : 0);
+                const int u = us + max(0, ue - uw);
+                if (u > 0) {
+                    if (lane == 0) sm.seg[n] = make_seg(p.own, 1, rb, tiles, u, us, uw - us, qa, c - qa, rend);
+                    ++n;
+                    tiles += (u + upt - 1) / upt;
                 }
             }
             qa = c;
@@ -247,23 +353,30 @@ __global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
             sm.nseg = n;
             sm.ntiles = tiles;
         }
-    } else if (warp < 4) {
-        // Q: a warp per row; 16 channels per lane -> E4M3 hi and lo, scaled so that the row's largest is in [2^7, 2^8)
-        for (int r = warp; r < R; r += 4) {
-            const int c = r >> 4, h = r & 15;
-            uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    } else if (warp < kProducer) {
+        // Q: a warp per row; 16 channels per lane -> E4M3 hi and lo, scaled so that the row's largest is in [2^7, 2^8).
+        // All of a warp's rows are loaded before the first is converted.
+        uint4 v[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = warp + 4 * NQ * k, c = r >> 4;
+            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
             if (c < nq) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(f0 + c) * kH + h) * kD) + 2 * lane;
-                v[0] = __ldg(src);
-                v[1] = __ldg(src + 1);
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(f0 + c) * kH + (r & 15)) * kD) + 2 * lane;
+                v[k][0] = __ldg(src);
+                v[k][1] = __ldg(src + 1);
             }
-            const float mx = redux_max(fmaxf(bf16x8_maxabs(v[0]), bf16x8_maxabs(v[1])));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = warp + 4 * NQ * k, c = r >> 4, h = r & 15;
+            const float mx = redux_max(fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1])));
             const int e = max((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127 - 7, -120);
             const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4& vv = v[j >> 1];
+                const uint4& vv = v[k][j >> 1];
                 const uint32_t w0 = (j & 1) ? vv.z : vv.x, w1 = (j & 1) ? vv.w : vv.y;
                 const float x[4] = {__uint_as_float(w0 << 16) * mul, __uint_as_float(w0 & 0xFFFF0000u) * mul,
                                     __uint_as_float(w1 << 16) * mul, __uint_as_float(w1 & 0xFFFF0000u) * mul};
@@ -288,362 +401,333 @@ __global__ void __launch_bounds__(kThreads, (NQ == 1 && ST == 1) ? 2 : 1)
     }
     fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();
+    if (warp == kProducer) {   // needs nothing of the others: its copies go out while Q is converted
+        __syncwarp();
+        asm volatile("bar.arrive 15, %0;" ::"n"(kWg * NQ + 64) : "memory");
+    } else {
+        asm volatile("bar.sync 15, %0;" ::"n"(kWg * NQ + 64) : "memory");
+    }
     tc_fence_after();
-    const uint32_t tmem = sm.tmem;
+    const uint32_t tmem = warp == kProducer ? 0u : sm.tmem;
     const int ntiles = sm.ntiles;
-    const int t0 = (int)((int64_t)ntiles * blockIdx.x / args.splits), t1 = (int)((int64_t)ntiles * (blockIdx.x + 1) / args.splits);
+    const int t0 = first_tile(ntiles, blockIdx.x), t1 = first_tile(ntiles, blockIdx.x + 1), nt = t1 - t0;
 
-    // A bounded wait; the first to run out of time tells every other.
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t start = globaltimer_ns();
-        for (uint32_t it = 1;; ++it) {
-            if (mbar_try_wait(bar, parity)) return true;
-            if ((it & 63u) == 0u) {
-                if (*(volatile int*)&sm.dead) return false;
-                if (globaltimer_ns() - start > kTimeoutNs) {
-                    *(volatile int*)&sm.dead = 1;
-                    if (p.flag) *p.flag = 1;
-                    return false;
-                }
-            }
-        }
-    };
-    auto seg_of = [&](int tile) -> int {
-        int s = 0;
-        while (s + 1 < sm.nseg && tile >= sm.seg[s + 1].tile0) ++s;
-        return s;
-    };
-
-    if (warp == 4) {
-        // ---- producer: one lane per 8-key group ----
-        int issued = 0;
-        bool ok = true;
-        for (int t = t0; t < t1; ++t) {
-            const int n = t - t0, st = n % ST;
-            const Seg& sg = sm.seg[seg_of(t)];
-            const csa2_pages& pg = sg.which ? p.own : p.prefix;
-            const int v = (t - sg.tile0) * kTileGroups + lane;
-            int row = -1;
-            if (lane < kTileGroups && v < sg.groups) {
-                const int slot = (v < sg.sink ? v : v + sg.delta) * kGroup;
-                const int page = pg.table[(int64_t)sg.b * pg.max_pages + slot / pg.page_size];
-                if (page >= 0 && page < pg.n_pages) row = page * pg.page_size + slot % pg.page_size;
-            }
-            const uint32_t live = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
-            if (n >= ST) ok = wait(&sm.empty[st], (uint32_t)((n / ST - 1) & 1));
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], live * kGroup * kD);
-            __syncwarp();
-            if (row >= 0 && !args.test_starve)
-                tma_group(sm.K[st] + lane * kGroup * kD, sg.which ? &map_own : &map_prefix, row / kGroup, &sm.full[st]);
-            ++issued;
-        }
+    if (warp == kProducer) {
+        int n = 0;
+        while (n < nt && load_tile(t0 + n, n)) ++n;
         if (*(volatile int*)&sm.dead) {   // wind down: the copies in flight land before the CTA ends
-            for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait(&sm.full[n % ST], (uint32_t)((n / ST) & 1));
+            for (int k = max(0, n - ST + 1); k <= min(n, nt - 1); ++k)
+                for (int c = 0; c < kBlocks; ++c) mbar_wait(&sm.full[k % ST][c], (uint32_t)((k / ST) & 1), kTimeoutNs / 8);
         }
-    } else if (warp == 5) {
-        // ---- MMA issuer (one lane): S of the next tile or O of the last, whichever is ready ----
-        if (lane == 0) {
-            const uint32_t sQ = smem_u32(sm.Qs), sP = smem_u32(sm.P);
-            const int n = t1 - t0;
-            int iq = 0, ip = 0;
-            uint64_t start = globaltimer_ns();
-            uint32_t idle = 0;
-            while (ip < n) {
-                bool moved = false;
-                if (iq < n && iq <= ip + 1 && mbar_try_wait(&sm.full[iq % ST], (uint32_t)((iq / ST) & 1))) {
-                    const Seg& sg = sm.seg[seg_of(t0 + iq)];
-                    const uint32_t k = smem_u32(sm.K[iq % ST]), d = tmem + kS0 + (iq & 1) * 2 * R + 32 * sg.qa;
-                    const uint32_t id = idesc_qk(32 * sg.nq);
+    } else if (warp == kIssuer) {
+        // ---- MMA issuer: a channel block of the next tile's S, or the last tile's O, whichever is ready ----
+        const uint32_t lead = elect_one();
+        const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t k0 = smem_u32(sm.K[0][0]);
+        const uint64_t qd = smem_desc(smem_u32(sm.Qs), 16, 1024, kSw128), pd = smem_desc(smem_u32(sm.P), 128, 2048, kLayoutNone);
+        // The products are unrolled: a loop around a few of them costs more than they do.
+        auto tile_seg = [&](int t, int& qa, int& qn, int& steps) {
+            const Seg& sg = sm.seg[seg_of(t)];
+            qa = __shfl_sync(0xFFFFFFFFu, sg.qa, 0);
+            qn = __shfl_sync(0xFFFFFFFFu, sg.nq, 0);
+            steps = (min(kTileKeys, __shfl_sync(0xFFFFFFFFu, (sg.units - (t - sg.tile0) * upt) * unit, 0)) + 31) / 32;   // of 32 keys
+        };
+        int iq = 0, ip = 0;   // next S tile, next O tile
+        uint64_t start = globaltimer_ns();
+        uint32_t idle = 0;
+        while (ip < nt) {
+            bool moved = false;
+            if (iq < nt && iq <= ip + 1 && mbar_test(&sm.full[iq % ST][0], (uint32_t)((iq / ST) & 1))) {
+                int qa, qn, steps;
+                tile_seg(t0 + iq, qa, qn, steps);
+                const uint64_t a = smem_desc(k0 + (iq % ST) * (kBlocks * kBlockBytes), 16, 1024, kSw128), b = qd + qa * (4096 / 16);
+                const uint32_t d = td + kS0 + (iq & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+#pragma unroll
+                for (int c = 0; c < kBlocks; ++c) {
+                    if (c > 0) wait(&sm.full[iq % ST][c], (uint32_t)((iq / ST) & 1));
                     tc_fence_after();
 #pragma unroll
-                    for (int s = 0; s < kD / 32; ++s)
-                        mma_f8(d, smem_desc(k + (s >> 2) * 1024 + (s & 3) * 32, 16, 4096, kSw128),
-                               smem_desc(sQ + (s >> 2) * (2 * R * 128) + sg.qa * 4096 + (s & 3) * 32, 16, 1024, kSw128), id, s > 0);
-                    tc_commit(&sm.s_full[iq & 1]);
-                    ++iq;
-                    moved = true;
+                    for (int s = 0; s < 4; ++s)
+                        mma_f8(lead, d, a + (c * kBlockBytes + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
                 }
-                if (ip < iq && mbar_try_wait(&sm.p_full, (uint32_t)(ip & 1))) {
-                    const int t = t0 + ip;
-                    const Seg& sg = sm.seg[seg_of(t)];
-                    const uint32_t k = smem_u32(sm.K[ip % ST]);
-                    const int keys = min(kTileGroups, sg.groups - (t - sg.tile0) * kTileGroups) * kGroup;
-                    const int steps = (keys + 31) / 32;
-                    tc_fence_after();
-                    for (int s = 0; s < steps; ++s) {
+                commit(lead, &sm.s_full[iq & 1]);
+                ++iq;
+                moved = true;
+            } else if (ip < iq && mbar_test(&sm.p_full, (uint32_t)(ip & 1))) {
+                int qa, qn, steps;
+                tile_seg(t0 + ip, qa, qn, steps);
+                const uint64_t a = smem_desc(k0 + (ip % ST) * (kBlocks * kBlockBytes), 16, 1024, kSw128);
+                tc_fence_after();
+                if (kConcat && qn == NQ) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            const uint64_t a = smem_desc(k + s * 16384 + b * 1024, 1024, 4096, kSw128);
-                            const uint32_t d = tmem + b * kOCols + kH * sg.qa;
-                            if (kConcat && sg.nq == NQ) {
-                                mma_f8(d, a, smem_desc(sP + s * 512, 128, 2048, kLayoutNone), idesc_pv(3 * R), 1);
-                            } else {
+                    for (int c = 0; c < kBlocks; ++c) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (s < steps)
+                                mma_f8(lead, td + c * kOCols, a + (c * kBlockBytes + s * 4096) / 16, pd + s * (512 / 16), idesc_pv(3 * R), 1);
+                        commit(lead, &sm.empty[ip % ST][c]);   // the block's memory is free for the next tile
+                    }
+                } else {
+                    const uint64_t b = pd + qa * (2048 / 16);
+                    const uint32_t id = idesc_pv(kH * qn), d = td + kH * qa;
+#pragma unroll
+                    for (int c = 0; c < kBlocks; ++c) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            if (s < steps)
 #pragma unroll
                                 for (int x = 0; x < 3; ++x)
-                                    mma_f8(d + (kConcat ? x * R : 0), a,
-                                           smem_desc(sP + (x * NQ + sg.qa) * 2048 + s * 512, 128, 2048, kLayoutNone),
-                                           idesc_pv(kH * sg.nq), 1);
-                            }
-                        }
-                    }
-                    tc_commit(&sm.empty[ip % ST]);
-                    tc_commit(&sm.pv_done);
-                    ++ip;
-                    moved = true;
-                }
-                if (moved) {
-                    idle = 0;
-                } else if ((++idle & 63u) == 0u) {
-                    if (idle == 64u) start = globaltimer_ns();
-                    if (*(volatile int*)&sm.dead) break;
-                    if (globaltimer_ns() - start > kTimeoutNs) {
-                        *(volatile int*)&sm.dead = 1;
-                        if (p.flag) *p.flag = 1;
-                        break;
+                                    mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), a + (c * kBlockBytes + s * 4096) / 16,
+                                           b + (x * NQ * 2048 + s * 512) / 16, id, 1);
+                        commit(lead, &sm.empty[ip % ST][c]);
                     }
                 }
+                commit(lead, &sm.pv_done);
+                ++ip;
+                moved = true;
             }
-            if (*(volatile int*)&sm.dead) {   // wind down: no MMA in flight when TMEM is freed
-                tc_commit(&sm.wind_down);
-                mbar_wait(&sm.wind_down, 0);
+            if (moved) {
+                idle = 0;
+            } else if ((++idle & 63u) == 0u) {
+                if (idle == 64u) start = globaltimer_ns();
+                const bool late = globaltimer_ns() - start > kTimeoutNs;
+                if (late && lead) {
+                    *(volatile int*)&sm.dead = 1;
+                    if (p.flag) *p.flag = 1;
+                }
+                if (__any_sync(0xFFFFFFFFu, late || *(volatile int*)&sm.dead)) break;
             }
+        }
+        if (__any_sync(0xFFFFFFFFu, *(volatile int*)&sm.dead)) {   // wind down: no MMA in flight when TMEM is freed
+            commit(lead, &sm.wind_down);
+            mbar_wait(&sm.wind_down, 0);
         }
         __syncwarp();
     } else {
-        // ---- softmax: thread = key ----
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        // ---- softmax: warpgroup = query, thread = key ----
+        const int wg = warp >> 2, key = tid & (kWg - 1), quarter = warp & 3;
+        const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int qi = sm.qi[wg], qlow = sm.qlow[wg];
+        // this query's accumulator columns: 16 of each channel block (and of each term)
+        auto ocol = [&](int b, int x) -> uint32_t { return tq + b * kOCols + x * R + kH * wg; };
+        constexpr int kTerms = kConcat ? 3 : 1;
         {
-            uint32_t z[16] = {};
-            for (uint32_t c = 0; c < kS0; c += 16) tmem_st_x16(tmem + lanes + c, z);
+            uint32_t zero[16] = {};
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
             tmem_st_wait();
         }
-        float l[R];
+        float l[kH];
 #pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = 0.0f;
+        for (int h = 0; h < kH; ++h) l[h] = 0.0f;
+        auto row4 = [&](const float (&a)[R], int j) { return *reinterpret_cast<const float4*>(&a[kH * wg + 4 * j]); };
+        const int ku = key / unit, ko = key % unit;
 
-        // the thread's key of a tile: its row in the pool, or -1, and which queries see it
-        auto key_of = [&](int t, int& row, uint32_t& vis, const float*& scales) {
-            const Seg& sg = sm.seg[seg_of(t)];
-            const csa2_pages& pg = sg.which ? p.own : p.prefix;
-            scales = pg.kv_sc;
-            row = -1;
-            vis = 0;
-            const int v = (t - sg.tile0) * kTileGroups + (tid >> 3);
-            if (v >= sg.groups) return;
-            const int slot = (v < sg.sink ? v : v + sg.delta) * kGroup + (tid & 7), pos = pg.pos0 + slot;
-            if (pos >= sg.end) return;
-            const int page = pg.table[(int64_t)sg.b * pg.max_pages + slot / pg.page_size];
-            if (page < 0 || page >= pg.n_pages) return;
-            row = page * pg.page_size + slot % pg.page_size;
-#pragma unroll
-            for (int c = 0; c < NQ; ++c)
-                if (c >= sg.qa && c < sg.qa + sg.nq && pos <= sm.qi[c] && (pos >= sm.qlow[c] || (sg.which && pos < p.n_sink)))
-                    vis |= 1u << c;
-        };
-        int row = -1;
-        uint32_t vis = 0;
-        float ts = 0.0f;
-        const float* scales = nullptr;
-        if (t0 < t1) {
-            key_of(t0, row, vis, scales);
-            if (vis) ts = __ldg(scales + row);
-        }
         // After a wait that ran out the loop goes on with what is there: every thread passes every barrier.
-        for (int t = t0; t < t1; ++t) {
-            const int n = t - t0;
-            int nrow = -1;
-            uint32_t nvis = 0;
-            const float* nscales = nullptr;
-            if (t + 1 < t1) key_of(t + 1, nrow, nvis, nscales);
+        for (int n = 0; n < nt; ++n) {
+            const int t = t0 + n, st = n % ST;
             const Seg& sg = sm.seg[seg_of(t)];
-            const int keys = min(kTileGroups, sg.groups - (t - sg.tile0) * kTileGroups) * kGroup;
-            const float lsc = fmaxf(__log2f(ts), kMinLogScale);
+            const int v = (t - sg.tile0) * upt + ku, left = (sg.units - (t - sg.tile0) * upt) * unit;
+            const int pos = sg.pos0 + sg.unit(v) * unit + ko;
+            const bool active = wg >= sg.qa && wg < sg.qa + sg.nq;   // this tile's products cover this query
+            const bool sink = sg.own && pos < p.n_sink;
+            wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));         // the scales
+            const bool stored = v < sg.units && pos < sg.end && sm.held[st][ku];
+            const bool seen = stored && active && pos <= qi && (pos >= qlow || sink);
+            const float ts = seen ? sm.sc[st][key] : 0.0f;
+            // a key that no query of the CTA sees, within the steps that P K takes: its row will be zeroed
+            bool unseen = key < ((min(kTileKeys, left) + 31) & ~31);
+            if (stored)
+                for (int c = sg.qa; c < sg.qa + sg.nq; ++c) unseen &= !(pos <= sm.qi[c] && (pos >= sm.qlow[c] || sink));
             wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1));
             tc_fence_after();
-            float z[R];
-            const uint32_t sbase = tmem + lanes + kS0 + (n & 1) * 2 * R;
+            if (active) {
+                const float lsc = fmaxf(__log2f(ts), kMinLogScale);
+                float z[kH], x[kH];   // z = q . k; x = z in log2 units less the row's reference
+                {
+                    uint32_t u[32];
+                    tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * R + 32 * wg, u);
+                    tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < NQ; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(sbase + 32 * c, v);
-                tmem_ld_wait();
+                    for (int h = 0; h < kH; ++h) z[h] = (__uint_as_float(u[h]) + __uint_as_float(u[16 + h])) * ts;
+                }
+                auto relative = [&]() {   // the product rounded first, as in the maximum: huge logits still meet it exactly
 #pragma unroll
-                for (int h = 0; h < kH; ++h) z[16 * c + h] = __uint_as_float(v[h]) + __uint_as_float(v[16 + h]);
-            }
-            tc_fence_before();
-            // logits (log2 units), and each row's maximum of z + log2(scale) over the warp's keys
-#pragma unroll
-            for (int c = 0; c < NQ; ++c) {
-                const bool seen = (vis >> c) & 1u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sm.rowf[16 * c + 4 * j]);
-                    const float ff[4] = {f.x, f.y, f.z, f.w};
-                    float mx[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 16 * c + 4 * j + i;
-                        z[r] = seen ? z[r] * ts * ff[i] : -INFINITY;
-                        mx[i] = redux_max(z[r] + lsc);
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 f = row4(sm.rowf, j), m = row4(sm.mref, j);
+                        x[4 * j] = __fmul_rn(z[4 * j], f.x) - m.x;
+                        x[4 * j + 1] = __fmul_rn(z[4 * j + 1], f.y) - m.y;
+                        x[4 * j + 2] = __fmul_rn(z[4 * j + 2], f.z) - m.z;
+                        x[4 * j + 3] = __fmul_rn(z[4 * j + 3], f.w) - m.w;
                     }
-                    if (lane == 0) *reinterpret_cast<float4*>(&sm.wmax[warp][16 * c + 4 * j]) = make_float4(mx[0], mx[1], mx[2], mx[3]);
-                }
-            }
-            softmax_bar();
-            if (tid < R) {
-                const float m = fmaxf(fmaxf(sm.wmax[0][tid], sm.wmax[1][tid]), fmaxf(sm.wmax[2][tid], sm.wmax[3][tid]));
-                const float old = sm.mref[tid];
-                float f = 1.0f;
-                if (m > old + kHeadroom) {   // -inf + 3 is -inf: a row's first keys always set it
-                    f = old == -INFINITY ? 0.0f : ex2(old - m);
-                    sm.mref[tid] = m;
-                    sm.rescale[n & 1] = 1;
-                }
-                sm.fac[tid] = f;
-            }
-            if (tid == 0) sm.rescale[(n + 1) & 1] = 0;
-            softmax_bar();
-            if (nvis) nscales += nrow;
-            const float nts = nvis ? __ldg(nscales) : 0.0f;
-            if (sm.rescale[n & 1]) {
-                if (n > 0) {
-                    wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int col = 0; col < (int)kS0; col += 16) {
-                        uint32_t o[16];
-                        tmem_ld_32x32b_x16(tmem + lanes + col, o);
-                        tmem_ld_wait();
-                        const float* fc = &sm.fac[col % R];
+                    if (!__all_sync(0xFFFFFFFFu, seen)) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fc[i]);
-                        tmem_st_x16(tmem + lanes + col, o);
+                        for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
                     }
-                    tmem_st_wait();
+                };
+                relative();
+                float top = x[0];
+#pragma unroll
+                for (int h = 1; h < kH; ++h) top = fmaxf(top, x[h]);
+                // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
+                if (wg_any(wg, top + lsc > kHeadroom)) {
+                    float mx[kH];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 f4 = row4(sm.rowf, j);
+                        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx[4 * j + i] = redux_max(seen ? __fmul_rn(z[4 * j + i], f[i]) + lsc : -INFINITY);
+                    }
+                    if (lane == 0) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4*>(&sm.wmax[quarter][kH * wg + 4 * j]) =
+                                make_float4(mx[4 * j], mx[4 * j + 1], mx[4 * j + 2], mx[4 * j + 3]);
+                    }
+                    wg_bar(wg);
+                    if (key < kH) {
+                        const int r = kH * wg + key;
+                        const float m = fmaxf(fmaxf(sm.wmax[0][r], sm.wmax[1][r]), fmaxf(sm.wmax[2][r], sm.wmax[3][r]));
+                        const float old = sm.mref[r];
+                        sm.fac[r] = m > old ? (old == -INFINITY ? 0.0f : ex2(old - m)) : 1.0f;
+                        sm.mref[r] = fmaxf(m, old);
+                    }
+                    wg_bar(wg);
+                    if (n > 0) {
+                        wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+                        tc_fence_after();
+#pragma unroll
+                        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                            for (int y = 0; y < kTerms; ++y) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(ocol(b, y), o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int h = 0; h < kH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sm.fac[kH * wg + h]);
+                                tmem_st_x16(ocol(b, y), o);
+                            }
+                        tmem_st_wait();
+                    }
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
+                    relative();
                 }
-#pragma unroll
-                for (int r = 0; r < R; ++r) l[r] *= sm.fac[r];
-            }
-            const float tp = ts * kPScale;
-#pragma unroll
-            for (int j = 0; j < R / 4; ++j) {
-                const float4 m = *reinterpret_cast<const float4*>(&sm.mref[4 * j]);
-                const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 4 * j + i;
-                    // a row that has seen nothing has z and m at -inf: its weight is 0
-                    z[r] = z[r] == -INFINITY ? 0.0f : ex2(z[r] - mm[i]);
-                    l[r] += z[r];
-                }
-            }
-            if (n > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));   // P is free when the last tile's products are done
-#pragma unroll
-            for (int c = 0; c < NQ; ++c) {
+                const float tp = ts * kPScale;
                 uint32_t w[3][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    float e[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        e[i] = ex2(x[4 * j + i]);
+                        l[4 * j + i] += e[i];
+                    }
                     uint32_t h0, m0, l0, h1, m1, l1;
-                    split_e5m2(pack_f16(z[16 * c + 4 * j] * tp, z[16 * c + 4 * j + 1] * tp), h0, m0, l0);
-                    split_e5m2(pack_f16(z[16 * c + 4 * j + 2] * tp, z[16 * c + 4 * j + 3] * tp), h1, m1, l1);
+                    split_e5m2(pack_f16(e[0] * tp, e[1] * tp), h0, m0, l0);
+                    split_e5m2(pack_f16(e[2] * tp, e[3] * tp), h1, m1, l1);
                     w[0][j] = __byte_perm(h0, h1, 0x7531);
                     w[1][j] = __byte_perm(m0, m1, 0x7531);
                     w[2][j] = __byte_perm(l0, l1, 0x7531);
                 }
+                if (n > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));   // P is free when the last tile's products are done
 #pragma unroll
-                for (int x = 0; x < 3; ++x)
-                    *reinterpret_cast<uint4*>(&sm.P[x * NQ + c][tid][0]) = make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+                for (int y = 0; y < 3; ++y)
+                    *reinterpret_cast<uint4*>(&sm.P[y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+            } else if (n > 0) {
+                // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
+                wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
             }
-            if (!vis && tid < ((keys + 31) & ~31)) {   // S of this tile is done: its rows are read only by P K from here
-                uint8_t* krow = sm.K[n % ST] + (tid >> 3) * (kGroup * kD) + (tid & 7) * 128;
+            if (unseen) {   // S of this tile is done: only P K still reads the row
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int b = wg; b < kBlocks; b += NQ)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(krow + b * 1024 + 16 * ((j + tid) & 7)) = make_uint4(0, 0, 0, 0);
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(&sm.K[st][b][key * 128 + 16 * ((j + key) & 7)]) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(&sm.p_full);
-            row = nrow;
-            vis = nvis;
-            ts = nts;
         }
         // ---- row sums over the 128 threads, then the output ----
-        if (t1 > t0) wait(&sm.pv_done, (uint32_t)((t1 - t0 - 1) & 1));
-        tc_fence_after();
-        float* stage = reinterpret_cast<float*>(sm.K[0]);   // every copy and product is done: the tile is free
+        {
+            // halving exchange: after step o a lane holds the sums over lane pairs of half as many rows
+            float v[kH];
 #pragma unroll
-        for (int r = 0; r < R; ++r) stage[r * (kSoftmaxThreads + 1) + tid] = l[r];
-        softmax_bar();
-        if (tid < R) {
-            float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-            for (int k = 0; k < kSoftmaxThreads; k += 4)
+            for (int h = 0; h < kH; ++h) v[h] = l[h];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] += stage[tid * (kSoftmaxThreads + 1) + k + i];
-            sm.lsum[tid] = (a[0] + a[1]) + (a[2] + a[3]);
-        }
-        softmax_bar();
-        if (tid < R) {
-            const float sum = sm.lsum[tid], m = sm.mref[tid];
-            const int c = tid >> 4;
-            if (args.splits > 1) {
-                float* ml = args.part_ml + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + tid) * 2;
-                ml[0] = m;
-                ml[1] = sum;
-            } else if (p.lse && c < nq) {
-                p.lse[(int64_t)(f0 + c) * kH + (tid & 15)] = sum > 0.0f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-            }
-            sm.fac[tid] = (sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
-        }
-        softmax_bar();
-        uint16_t* ostage = reinterpret_cast<uint16_t*>(sm.K[0]);   // [R][512] bf16
-        float* po = args.part_o + ((int64_t)blockIdx.y * args.splits + blockIdx.x) * R * kD;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            const int dim = 128 * b + tid;
+            for (int o = 8; o > 0; o >>= 1) {
+                const bool up = (lane & o) != 0;
 #pragma unroll
-            for (int c = 0; c < NQ; ++c) {
-                float o[16];
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(tmem + lanes + b * kOCols + 16 * c, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(v[i]);
-                if (kConcat) {
-#pragma unroll
-                    for (int x = 1; x < 3; ++x) {
-                        tmem_ld_32x32b_x16(tmem + lanes + b * kOCols + x * R + 16 * c, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] += __uint_as_float(v[i]);
-                    }
+                for (int h = 0; h < o; ++h) {
+                    const float keep = up ? v[h + o] : v[h], give = up ? v[h] : v[h + o];
+                    v[h] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
                 }
+            }
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);   // lane i: row i & 15
+            wg_bar(wg);   // wmax of the last tile has been read
+            if (lane < kH) sm.wmax[quarter][kH * wg + lane] = v[0];
+        }
+        wg_bar(wg);
+        if (key < kH) {
+            const int r = kH * wg + key;
+            const float sum = (sm.wmax[0][r] + sm.wmax[1][r]) + (sm.wmax[2][r] + sm.wmax[3][r]), m = sm.mref[r];
+            if (args.splits > 1) {
+                float* ml = args.part_ml + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + r) * 2;
+                *reinterpret_cast<float2*>(ml) = make_float2(m, sum);
+            } else if (p.lse && wg < nq) {
+                p.lse[(int64_t)(f0 + wg) * kH + key] = sum > 0.0f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            }
+            sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
+        }
+        wg_bar(wg);
+        if (nt > 0) wait(&sm.pv_done, (uint32_t)((nt - 1) & 1));
+        tc_fence_after();
+        float fac[kH];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 f = row4(sm.fac, j);
+            fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
+        }
+        // every copy and product is done: the tiles' memory takes the query's [16][512] bf16
+        uint16_t* ostage = reinterpret_cast<uint16_t*>(&sm.K[0][0][0]) + wg * kH * kD;
+        float* po = args.part_o + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + kH * wg) * kD;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const int dim = 128 * b + key;
+            uint32_t o[kTerms][16];
+#pragma unroll
+            for (int y = 0; y < kTerms; ++y) tmem_ld_32x32b_x16(ocol(b, y), o[y]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+                float y = __uint_as_float(o[0][h]);
+#pragma unroll
+                for (int x = 1; x < kTerms; ++x) y += __uint_as_float(o[x][h]);
+                y *= fac[h];
                 if (args.splits > 1) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) po[(int64_t)(16 * c + i) * kD + dim] = o[i] * (1.0f / kPScale);
+                    po[h * kD + dim] = y;
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const __nv_bfloat16 h = __float2bfloat16_rn(o[i] * sm.fac[16 * c + i]);
-                        ostage[(16 * c + i) * kD + dim] = *reinterpret_cast<const uint16_t*>(&h);
-                    }
+                    const __nv_bfloat16 yb = __float2bfloat16_rn(y);
+                    ostage[h * kD + dim] = *reinterpret_cast<const uint16_t*>(&yb);
                 }
             }
         }
         if (args.splits == 1) {
-            softmax_bar();
+            wg_bar(wg);
             const uint4* src = reinterpret_cast<const uint4*>(ostage);
-            uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)f0 * kH * kD);
-            for (int j = tid; j < nq * kH * kD / 8; j += kSoftmaxThreads) dst[j] = src[j];
+            uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(f0 + wg) * kH * kD);
+            if (wg < nq)
+#pragma unroll
+                for (int j = 0; j < kH * kD / 8 / kWg; ++j) dst[key + kWg * j] = src[key + kWg * j];
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 5) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the splits of a block: one CTA per row, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).
@@ -730,15 +814,14 @@ EncodeFn encoder() {
     return fn;
 }
 
-// The pool as [group of 8 rows][4 blocks of 128 channels][8 rows][128 B]: a box is one group, in the
-// order in which the tile keeps it.
-cudaError_t pool_map(const csa2_pages& pg, CUtensorMap* map) {
+// The pool as [4 blocks of 128 channels][rows][128 B]: a box is one block of a unit's rows.
+cudaError_t pool_map(const csa2_pages& pg, int unit, CUtensorMap* map) {
     const EncodeFn fn = encoder();
     if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[4] = {128, kGroup, kD / 128, (cuuint64_t)(pg.n_pages * pg.page_size / kGroup)};
-    const cuuint64_t strides[3] = {kD, 128, (cuuint64_t)kGroup * kD};
-    const cuuint32_t box[4] = {128, kGroup, kD / 128, 1}, es[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t dims[3] = {128, (cuuint64_t)(pg.n_pages * pg.page_size), kBlocks};
+    const cuuint64_t strides[2] = {kD, 128};
+    const cuuint32_t box[3] = {128, (cuuint32_t)unit, 1}, es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
@@ -752,7 +835,7 @@ cudaError_t launch(const KernelArgs& a, int blocks, const CUtensorMap& own, cons
         return cudaFuncSetAttribute(pages_attn_kernel<NQ, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_ex(pages_attn_kernel<NQ, ST>, dim3(a.splits, blocks), dim3(kThreads), smem, st, 0, own, prefix, a);
+    return launch_ex(pages_attn_kernel<NQ, ST>, dim3(a.splits, blocks), dim3(kWg * NQ + 64), smem, st, 0, own, prefix, a);
 }
 
 }  // namespace
@@ -767,11 +850,15 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
     a.test_starve = test_starve_copies();
     a.part_o = (float*)ws;
     a.part_ml = (float*)((char*)ws + pl.o_bytes);
+    // Large boxes cost fewer copies; a window's first unit reaches back over up to unit - 1 keys that no query sees.
+    int unit = p.prefix.B || p.window >= 1024 ? 64 : 32;
+    while (p.own.page_size % unit || (p.prefix.B && p.prefix.page_size % unit)) unit /= 2;
+    a.unit = unit;
     CUtensorMap own, prefix;
-    cudaError_t e = pool_map(p.own, &own);
+    cudaError_t e = pool_map(p.own, unit, &own);
     if (e != cudaSuccess) return e;
     if (p.prefix.B) {
-        e = pool_map(p.prefix, &prefix);
+        e = pool_map(p.prefix, unit, &prefix);
         if (e != cudaSuccess) return e;
     } else {
         prefix = own;

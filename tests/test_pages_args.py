@@ -21,7 +21,7 @@ def pages(csa, **kw):
     return csa.csa2_pages(**a)
 
 
-BAD_PAGES = [dict(kv=None), dict(kv_sc=None), dict(table=None), dict(n_tokens=None), dict(kv=0x1008), dict(page_size=0),
+BAD_PAGES = [dict(kv=None), dict(kv_sc=None), dict(table=None), dict(n_tokens=None), dict(kv=0x1008), dict(kv_sc=0x1008), dict(page_size=0),
              dict(page_size=12), dict(page_size=8192), dict(B=0), dict(max_pages=0), dict(n_pages=0), dict(pos0=-1),
              dict(n_pages=1 << 26, page_size=64), dict(max_pages=1 << 25, page_size=64),
              dict(pos0=(1 << 31) - 10)]
