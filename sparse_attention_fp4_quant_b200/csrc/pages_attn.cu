@@ -50,6 +50,7 @@ struct Seg {
     int own;        // 0 = the shared prefix, 1 = a sequence's own pages
     int qa, nq;
     int pos0, end;  // position of slot 0, and of the first slot behind the stored tokens
+    int imin, lmax;  // every query of the list sees the stored tokens in [lmax, imin]
     int page_size, n_pages;
     const int32_t* table;   // the sequence's row
     const float* scales;
@@ -58,10 +59,17 @@ struct Seg {
 };
 
 __device__ __forceinline__ Seg make_seg(const csa2_pages& pg, int own, int b, int tile0, int units, int sink, int delta,
-                                        int qa, int nq, int end) {
-    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, pg.page_size, (int)pg.n_pages,
+                                        int qa, int nq, int end, int imin, int lmax) {
+    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, imin, lmax, pg.page_size, (int)pg.n_pages,
             pg.table + (int64_t)b * pg.max_pages, pg.kv_sc};
 }
+
+// What the roles need of a tile, written by the producer with its copies.
+struct __align__(16) Tile {
+    int qa, nq;     // queries
+    int steps;      // steps of 32 keys
+    int interior;   // every key is stored and seen by all of them
+};
 
 template <int NQ, int ST>
 struct Smem {
@@ -71,6 +79,7 @@ struct Smem {
     alignas(1024) uint8_t P[3 * NQ][kTileKeys][16];      // [term][query]: 16 rows of each key, no swizzle
     alignas(16) float sc[ST][kTileKeys];                 // the keys' token scales
     uint8_t held[ST][kTileKeys / kGroup];                // whether a unit's page exists
+    Tile tile[ST];
     alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
     alignas(16) float fac[R];
@@ -80,7 +89,7 @@ struct Smem {
     int qi[NQ], qlow[NQ];
     int dead;
     uint32_t tmem;
-    uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], p_full, pv_done, wind_down;
+    uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], s_free[2], p_full, pv_done, wind_down[2];
 };
 
 // The issuing warp runs its loop converged and one elected lane (lead != 0) issues: descriptors then stay in
@@ -97,17 +106,6 @@ __device__ __forceinline__ void mma_f8(uint32_t lead, uint32_t d, uint64_t a, ui
         "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
-}
-
-// Phase test that returns at once.  The issuer watches two barriers: a try_wait on one may sleep past the other.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
@@ -196,7 +194,7 @@ struct KernelArgs {
 };
 
 template <int NQ, int ST>
-__global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
+__global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
     pages_attn_kernel(const __grid_constant__ CUtensorMap map_own, const __grid_constant__ CUtensorMap map_prefix,
                       const __grid_constant__ KernelArgs args) {
     using Sm = Smem<NQ, ST>;
@@ -224,7 +222,10 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
         mbar_init(&sm.s_full[1], 1);
         mbar_init(&sm.p_full, kWg * NQ);
         mbar_init(&sm.pv_done, 1);
-        mbar_init(&sm.wind_down, 1);
+        mbar_init(&sm.wind_down[0], 1);
+        mbar_init(&sm.wind_down[1], 1);
+        mbar_init(&sm.s_free[0], 4 * NQ);
+        mbar_init(&sm.s_free[1], 4 * NQ);
         fence_mbar_init();
         sm.dead = 0;
     }
@@ -275,13 +276,20 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
             if (page >= 0 && page < sg.n_pages) row = page * sg.page_size + (slot - pg * sg.page_size);
         }
         const uint32_t live = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+        const int first = sg.pos0 + sg.unit(v) * unit, last = first + unit - 1;
+        const bool inside = row >= 0 && last < sg.end && last <= sg.imin && (first >= sg.lmax || (sg.own && last < p.n_sink));
+        const int keys = min(kTileKeys, (sg.units - (t - sg.tile0) * upt) * unit);
+        const Tile info = {sg.qa, sg.nq, (keys + 31) / 32, __popc(__ballot_sync(0xFFFFFFFFu, inside)) == upt};
         const CUtensorMap* map = sg.own ? &map_own : &map_prefix;
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) {
             bool ok = true;
             if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
-            if (c == 0 && lane < upt) sm.held[st][lane] = row >= 0;
+            if (c == 0) {
+                if (lane < upt) sm.held[st][lane] = row >= 0;
+                if (lane == 0) sm.tile[st] = info;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], live * unit * (c == 0 ? 128 + 4 : 128));
             __syncwarp();
@@ -308,15 +316,19 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
             sm.qi[lane] = i;
             sm.qlow[lane] = low;
         }
-        int n = 0, tiles = 0, imax = -1;
+        int n = 0, tiles = 0, imax = -1, imin = 0x7FFFFFFF;
 #pragma unroll
-        for (int c = 0; c < NQ; ++c) imax = max(imax, __shfl_sync(0xFFFFFFFFu, i, c));
+        for (int c = 0; c < NQ; ++c) {
+            const int ic = __shfl_sync(0xFFFFFFFFu, i, c);
+            imax = max(imax, ic);
+            if (c < nq) imin = min(imin, ic);
+        }
         if (shared_prefix) {
             pend = __shfl_sync(0xFFFFFFFFu, pend, 0);
             const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
             if (e > 0) {
                 const int u = (e + unit - 1) / unit;
-                if (lane == 0) sm.seg[n] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend);
+                if (lane == 0) sm.seg[n] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
                 ++n;
                 tiles = (u + upt - 1) / upt;
             }
@@ -324,9 +336,11 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
         int qa = 0;
         while (qa < nq) {   // runs of queries of one sequence
             const int rb = __shfl_sync(0xFFFFFFFFu, b, qa), rend = __shfl_sync(0xFFFFFFFFu, end, qa);
-            int c = qa, hi = 0, lo = 0x7FFFFFFF;
+            int c = qa, hi = 0, lo = 0x7FFFFFFF, rmin = 0x7FFFFFFF, rlow = 0;
             while (c < nq && __shfl_sync(0xFFFFFFFFu, b, c) == rb) {
                 const int ic = __shfl_sync(0xFFFFFFFFu, i, c), lc = __shfl_sync(0xFFFFFFFFu, low, c);
+                rmin = min(rmin, ic);
+                rlow = max(rlow, lc);
                 if (ic >= 0) {
                     hi = max(hi, ic < rend ? ic + 1 : rend);
                     lo = min(lo, lc);
@@ -342,7 +356,7 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
                 const int uw = max(us, lo > base ? (lo - base) / unit : 0);
                 const int u = us + max(0, ue - uw);
                 if (u > 0) {
-                    if (lane == 0) sm.seg[n] = make_seg(p.own, 1, rb, tiles, u, us, uw - us, qa, c - qa, rend);
+                    if (lane == 0) sm.seg[n] = make_seg(p.own, 1, rb, tiles, u, us, uw - us, qa, c - qa, rend, rmin, rlow);
                     ++n;
                     tiles += (u + upt - 1) / upt;
                 }
@@ -403,9 +417,9 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
     tc_fence_before();
     if (warp == kProducer) {   // needs nothing of the others: its copies go out while Q is converted
         __syncwarp();
-        asm volatile("bar.arrive 15, %0;" ::"n"(kWg * NQ + 64) : "memory");
+        asm volatile("bar.arrive 15, %0;" ::"n"(kWg * NQ + 96) : "memory");
     } else {
-        asm volatile("bar.sync 15, %0;" ::"n"(kWg * NQ + 64) : "memory");
+        asm volatile("bar.sync 15, %0;" ::"n"(kWg * NQ + 96) : "memory");
     }
     tc_fence_after();
     const uint32_t tmem = warp == kProducer ? 0u : sm.tmem;
@@ -420,87 +434,85 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
                 for (int c = 0; c < kBlocks; ++c) mbar_wait(&sm.full[k % ST][c], (uint32_t)((k / ST) & 1), kTimeoutNs / 8);
         }
     } else if (warp == kIssuer) {
-        // ---- MMA issuer: a channel block of the next tile's S, or the last tile's O, whichever is ready ----
+        // ---- S issuer.  S and O have a warp each: one thread issues a product in about 50 cycles, more than most of
+        // these take, and each stream's waits then leave the other alone.  A tile's products are unrolled.
         const uint32_t lead = elect_one();
         const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
         const uint32_t k0 = smem_u32(sm.K[0][0]);
-        const uint64_t qd = smem_desc(smem_u32(sm.Qs), 16, 1024, kSw128), pd = smem_desc(smem_u32(sm.P), 128, 2048, kLayoutNone);
-        // The products are unrolled: a loop around a few of them costs more than they do.
-        auto tile_seg = [&](int t, int& qa, int& qn, int& steps) {
-            const Seg& sg = sm.seg[seg_of(t)];
-            qa = __shfl_sync(0xFFFFFFFFu, sg.qa, 0);
-            qn = __shfl_sync(0xFFFFFFFFu, sg.nq, 0);
-            steps = (min(kTileKeys, __shfl_sync(0xFFFFFFFFu, (sg.units - (t - sg.tile0) * upt) * unit, 0)) + 31) / 32;   // of 32 keys
-        };
-        int iq = 0, ip = 0;   // next S tile, next O tile
-        uint64_t start = globaltimer_ns();
-        uint32_t idle = 0;
-        while (ip < nt) {
-            bool moved = false;
-            if (iq < nt && iq <= ip + 1 && mbar_test(&sm.full[iq % ST][0], (uint32_t)((iq / ST) & 1))) {
-                int qa, qn, steps;
-                tile_seg(t0 + iq, qa, qn, steps);
-                const uint64_t a = smem_desc(k0 + (iq % ST) * (kBlocks * kBlockBytes), 16, 1024, kSw128), b = qd + qa * (4096 / 16);
-                const uint32_t d = td + kS0 + (iq & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+        const uint64_t qd = smem_desc(smem_u32(sm.Qs), 16, 1024, kSw128);
+        bool ok = true;
+        for (int n = 0; n < nt && ok; ++n) {
+            const int st = n % ST;
+            if (n >= 2) ok = wait(&sm.s_free[n & 1], (uint32_t)((n / 2 - 1) & 1));
+            ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1)) && ok;
+            __syncwarp();
+            const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
+            const uint64_t a = smem_desc(k0 + st * (kBlocks * kBlockBytes), 16, 1024, kSw128), b = qd + qa * (4096 / 16);
+            const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c) {
+                if (c > 0) {
+                    ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
+                    __syncwarp();
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    mma_f8(lead, d, a + (c * kBlockBytes + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
+            }
+            commit(lead, &sm.s_full[n & 1]);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+        if (!ok) {   // wind down: no product in flight when TMEM is freed
+            commit(lead, &sm.wind_down[0]);
+            mbar_wait(&sm.wind_down[0], 0);
+        }
+        __syncwarp();
+    } else if (warp == kIssuer + 1) {
+        // ---- O issuer ----
+        const uint32_t lead = elect_one();
+        const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t k0 = smem_u32(sm.K[0][0]);
+        const uint64_t pd = smem_desc(smem_u32(sm.P), 128, 2048, kLayoutNone);
+        bool ok = true;
+        for (int n = 0; n < nt && ok; ++n) {
+            const int st = n % ST;
+            ok = wait(&sm.p_full, (uint32_t)(n & 1));
+            __syncwarp();
+            const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
+            const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
+            const uint64_t a = smem_desc(k0 + st * (kBlocks * kBlockBytes), 16, 1024, kSw128);
+            tc_fence_after();
+            if (kConcat && qn == NQ) {   // the three terms as one product
 #pragma unroll
                 for (int c = 0; c < kBlocks; ++c) {
-                    if (c > 0) wait(&sm.full[iq % ST][c], (uint32_t)((iq / ST) & 1));
-                    tc_fence_after();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_f8(lead, d, a + (c * kBlockBytes + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
+                        if (s < steps)
+                            mma_f8(lead, td + c * kOCols, a + (c * kBlockBytes + s * 4096) / 16, pd + s * (512 / 16), idesc_pv(3 * R), 1);
+                    commit(lead, &sm.empty[st][c]);   // the block's memory is free for a coming tile
                 }
-                commit(lead, &sm.s_full[iq & 1]);
-                ++iq;
-                moved = true;
-            } else if (ip < iq && mbar_test(&sm.p_full, (uint32_t)(ip & 1))) {
-                int qa, qn, steps;
-                tile_seg(t0 + ip, qa, qn, steps);
-                const uint64_t a = smem_desc(k0 + (ip % ST) * (kBlocks * kBlockBytes), 16, 1024, kSw128);
-                tc_fence_after();
-                if (kConcat && qn == NQ) {
+            } else {
+                const uint64_t b = pd + qa * (2048 / 16);
+                const uint32_t id = idesc_pv(kH * qn), d = td + kH * qa;
 #pragma unroll
-                    for (int c = 0; c < kBlocks; ++c) {
+                for (int c = 0; c < kBlocks; ++c) {
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            if (s < steps)
-                                mma_f8(lead, td + c * kOCols, a + (c * kBlockBytes + s * 4096) / 16, pd + s * (512 / 16), idesc_pv(3 * R), 1);
-                        commit(lead, &sm.empty[ip % ST][c]);   // the block's memory is free for the next tile
-                    }
-                } else {
-                    const uint64_t b = pd + qa * (2048 / 16);
-                    const uint32_t id = idesc_pv(kH * qn), d = td + kH * qa;
+                    for (int s = 0; s < 4; ++s)
+                        if (s < steps)
 #pragma unroll
-                    for (int c = 0; c < kBlocks; ++c) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            if (s < steps)
-#pragma unroll
-                                for (int x = 0; x < 3; ++x)
-                                    mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), a + (c * kBlockBytes + s * 4096) / 16,
-                                           b + (x * NQ * 2048 + s * 512) / 16, id, 1);
-                        commit(lead, &sm.empty[ip % ST][c]);
-                    }
+                            for (int x = 0; x < 3; ++x)
+                                mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), a + (c * kBlockBytes + s * 4096) / 16,
+                                       b + (x * NQ * 2048 + s * 512) / 16, id, 1);
+                    commit(lead, &sm.empty[st][c]);
                 }
-                commit(lead, &sm.pv_done);
-                ++ip;
-                moved = true;
             }
-            if (moved) {
-                idle = 0;
-            } else if ((++idle & 63u) == 0u) {
-                if (idle == 64u) start = globaltimer_ns();
-                const bool late = globaltimer_ns() - start > kTimeoutNs;
-                if (late && lead) {
-                    *(volatile int*)&sm.dead = 1;
-                    if (p.flag) *p.flag = 1;
-                }
-                if (__any_sync(0xFFFFFFFFu, late || *(volatile int*)&sm.dead)) break;
-            }
+            commit(lead, &sm.pv_done);
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
-        if (__any_sync(0xFFFFFFFFu, *(volatile int*)&sm.dead)) {   // wind down: no MMA in flight when TMEM is freed
-            commit(lead, &sm.wind_down);
-            mbar_wait(&sm.wind_down, 0);
+        if (!ok) {
+            commit(lead, &sm.wind_down[1]);
+            mbar_wait(&sm.wind_down[1], 0);
         }
         __syncwarp();
     } else {
@@ -527,20 +539,21 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
 
         // After a wait that ran out the loop goes on with what is there: every thread passes every barrier.
         for (int n = 0; n < nt; ++n) {
-            const int t = t0 + n, st = n % ST;
-            const Seg& sg = sm.seg[seg_of(t)];
-            const int v = (t - sg.tile0) * upt + ku, left = (sg.units - (t - sg.tile0) * upt) * unit;
-            const int pos = sg.pos0 + sg.unit(v) * unit + ko;
-            const bool active = wg >= sg.qa && wg < sg.qa + sg.nq;   // this tile's products cover this query
-            const bool sink = sg.own && pos < p.n_sink;
-            wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));         // the scales
-            const bool stored = v < sg.units && pos < sg.end && sm.held[st][ku];
-            const bool seen = stored && active && pos <= qi && (pos >= qlow || sink);
+            const int st = n % ST;
+            wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
+            const Tile tile = sm.tile[st];
+            const bool active = wg >= tile.qa && wg < tile.qa + tile.nq;   // this tile's products cover this query
+            bool seen = active, unseen = false;   // by this query; by none of the CTA, within the steps that P K takes
+            if (!tile.interior) {
+                const Seg& sg = sm.seg[seg_of(t0 + n)];
+                const int v = (t0 + n - sg.tile0) * upt + ku, pos = sg.pos0 + sg.unit(v) * unit + ko;
+                const bool stored = v < sg.units && pos < sg.end && sm.held[st][ku], sink = sg.own && pos < p.n_sink;
+                seen = active && stored && pos <= qi && (pos >= qlow || sink);
+                unseen = key < 32 * tile.steps;
+                if (stored)
+                    for (int c = sg.qa; c < sg.qa + sg.nq; ++c) unseen &= !(pos <= sm.qi[c] && (pos >= sm.qlow[c] || sink));
+            }
             const float ts = seen ? sm.sc[st][key] : 0.0f;
-            // a key that no query of the CTA sees, within the steps that P K takes: its row will be zeroed
-            bool unseen = key < ((min(kTileKeys, left) + 31) & ~31);
-            if (stored)
-                for (int c = sg.qa; c < sg.qa + sg.nq; ++c) unseen &= !(pos <= sm.qi[c] && (pos >= sm.qlow[c] || sink));
             wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1));
             tc_fence_after();
             if (active) {
@@ -553,6 +566,9 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
 #pragma unroll
                     for (int h = 0; h < kH; ++h) z[h] = (__uint_as_float(u[h]) + __uint_as_float(u[16 + h])) * ts;
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.s_free[n & 1]);
                 auto relative = [&]() {   // the product rounded first, as in the maximum: huge logits still meet it exactly
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -562,7 +578,7 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
                         x[4 * j + 2] = __fmul_rn(z[4 * j + 2], f.z) - m.z;
                         x[4 * j + 3] = __fmul_rn(z[4 * j + 3], f.w) - m.w;
                     }
-                    if (!__all_sync(0xFFFFFFFFu, seen)) {
+                    if (!tile.interior) {
 #pragma unroll
                         for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
                     }
@@ -572,7 +588,7 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
 #pragma unroll
                 for (int h = 1; h < kH; ++h) top = fmaxf(top, x[h]);
                 // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
-                if (wg_any(wg, top + lsc > kHeadroom)) {
+                if (__builtin_expect(wg_any(wg, top + lsc > kHeadroom), 0)) {
                     float mx[kH];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -641,6 +657,7 @@ __global__ void __launch_bounds__(kWg * NQ + 64, (NQ == 1 && ST == 1) ? 2 : 1)
                 // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
                 wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
             }
+            if (!active && lane == 0) mbar_arrive(&sm.s_free[n & 1]);
             if (unseen) {   // S of this tile is done: only P K still reads the row
 #pragma unroll
                 for (int b = wg; b < kBlocks; b += NQ)
@@ -835,7 +852,7 @@ cudaError_t launch(const KernelArgs& a, int blocks, const CUtensorMap& own, cons
         return cudaFuncSetAttribute(pages_attn_kernel<NQ, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_ex(pages_attn_kernel<NQ, ST>, dim3(a.splits, blocks), dim3(kWg * NQ + 64), smem, st, 0, own, prefix, a);
+    return launch_ex(pages_attn_kernel<NQ, ST>, dim3(a.splits, blocks), dim3(kWg * NQ + 96), smem, st, 0, own, prefix, a);
 }
 
 }  // namespace
