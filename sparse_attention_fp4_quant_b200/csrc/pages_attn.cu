@@ -18,8 +18,8 @@
 // reference is the maximum of z + log2(token scale), the size of what enters P, and it moves
 // only when a tile exceeds it by 2^3 (P keeps that much room), so the accumulators are
 // rescaled rarely.  l = sum 2^(z - m) stays in fp32 registers.
-// Keys that no query of the CTA sees have their rows zeroed in shared memory before P K:
-// a slot may hold NaN bytes, and 0 times NaN is NaN.
+// A slot that no query sees may hold NaN bytes, and a weight of 0 times NaN is NaN.  Such a key's
+// S is NaN as well, so its thread finds out for nothing, and zeroes the row before P K.
 #include <cuda.h>
 
 #include "attn_common.cuh"
@@ -33,13 +33,14 @@ using namespace tc;
 
 constexpr int kTileKeys = 128;
 constexpr int kGroup = 8;                              // keys of one swizzle atom
-constexpr int kBlocks = kD / 128;                      // channel blocks: 128 channels of the tile's keys, 16 KB
-constexpr int kBlockBytes = kTileKeys * 128;
+constexpr int kBlocks = kD / 128;                      // channel blocks of 128 channels: 128 bytes, a swizzle row
+constexpr int kTileBytes = kTileKeys * kD;             // 64 KB
 constexpr int kWg = 128;                               // threads of a softmax warpgroup: one query, a thread per key
 constexpr float kHeadroom = 3.0f;                      // log2 of how far a weight may exceed the reference
 constexpr float kPScale = 4096.0f;                     // weight 1 at 2^12, 2^15 with the headroom: below f16's and E5M2's largest
 constexpr float kMinLogScale = -100.0f;                // token scales below 2^-100 count as 2^-100 in the reference
 constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kMaxSplits = 2 * kSplitSMs;
 
 // One list of keys of a CTA, for its queries [qa, qa + nq): units of `unit` slots of one table row (a unit is
 // one TMA box, inside one page), `sink` first units and then the window's (virtual unit v is unit v, or
@@ -69,16 +70,32 @@ struct __align__(16) Tile {
     int qa, nq;     // queries
     int steps;      // steps of 32 keys
     int interior;   // every key is stored and seen by all of them
+    int end, sink;  // first position behind the stored tokens; positions below sink stay visible
+    int pad[2];
+};
+
+// A tile lies in shared memory, moves and is freed in four parts, in one of two orders of its 8-key x 128-byte
+// swizzle atoms:
+//   by channels  [4 channel blocks][16 key groups]: a part is a channel block.  S takes a part as it lands, and O
+//                frees one while the next is in work, so the wait for the next tile is short; a copy moves one
+//                channel block of a unit, which pays for units of 64 keys and more.
+//   by keys      [16 key groups][4 channel blocks]: a part is 32 keys.  One copy moves all channels of a unit: with
+//                pages of 16 tokens a tile takes 1,060 cycles to fetch, against 2,340 by channels.
+template <bool kByKeys>
+struct Layout {
+    static constexpr uint32_t group = kByKeys ? 4096 : 1024;      // from one 8-key group to the next
+    static constexpr uint32_t block = kByKeys ? 1024 : 16384;     // from one channel block to the next
+    static constexpr uint32_t step = 4 * group;                   // 32 keys
 };
 
 template <int NQ, int ST>
 struct Smem {
     static constexpr int R = kH * NQ;
-    alignas(1024) uint8_t K[ST][kBlocks][kBlockBytes];   // [channel block][key][128 B], 128-byte swizzle
+    alignas(1024) uint8_t K[ST][kTileBytes];
     alignas(1024) uint8_t Qs[kBlocks][2 * R][128];       // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
     alignas(1024) uint8_t P[3 * NQ][kTileKeys][16];      // [term][query]: 16 rows of each key, no swizzle
     alignas(16) float sc[ST][kTileKeys];                 // the keys' token scales
-    uint8_t held[ST][kTileKeys / kGroup];                // whether a unit's page exists
+    int upos[ST][kTileKeys / kGroup];                    // position of each unit's first key, or one behind all where it has no page
     Tile tile[ST];
     alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
@@ -124,12 +141,20 @@ __device__ __forceinline__ uint32_t idesc_pv(int N) {
 }
 constexpr uint32_t kSw128 = 2;
 
-// 128 channels (block c) of one unit's rows.
+// Channel block c of one unit's rows, or all channels of one unit's 8-key groups.
 __device__ __forceinline__ void tma_unit(void* dst, const CUtensorMap* map, int row, int c, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
         "[%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(0), "r"(row), "r"(c), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_groups(void* dst, const CUtensorMap* map, int group, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(0), "r"(group), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -186,22 +211,24 @@ __device__ __forceinline__ int stored_end(const csa2_pages& pg, int b) {
 
 struct KernelArgs {
     PagesAttnParams p;
-    int unit;         // keys of a TMA box: 8 .. 128, divides every page
+    int unit_log2;    // keys of a TMA box: 8 .. 128, divides every page
     int splits;
     int test_starve;  // test hook (csa2_test_starve_copies): the producer issues no copies
     float* part_o;    // [block][split][R][512]
     float* part_ml;   // [block][split][R][2]
 };
 
-template <int NQ, int ST>
-__global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
+// NQ queries, ST tiles in flight, the order of a tile's atoms, whether the three terms of P have accumulator columns
+// of their own (one product for all three, 3R columns, where TMEM has room), CTAs on an SM.
+template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas>
+__global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
     pages_attn_kernel(const __grid_constant__ CUtensorMap map_own, const __grid_constant__ CUtensorMap map_prefix,
                       const __grid_constant__ KernelArgs args) {
     using Sm = Smem<NQ, ST>;
     constexpr int R = Sm::R;
-    constexpr bool kConcat = NQ <= 2;                  // the three terms of P in columns of their own (TMEM has room)
+    using L = Layout<kByKeys>;
     constexpr int kOCols = (kConcat ? 3 : 1) * R;      // accumulator columns of one channel block
-    constexpr uint32_t kTmemCols = NQ == 1 ? 256 : 512;
+    constexpr uint32_t kTmemCols = 512 / kCtas;
     constexpr uint32_t kS0 = 4 * kOCols;               // S^T buffers behind the accumulators
     static_assert(kS0 + 2 * 2 * R <= kTmemCols, "TMEM budget");
     extern __shared__ uint8_t smem_raw[];
@@ -209,13 +236,13 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
     const PagesAttnParams& p = args.p;
     constexpr int kProducer = 4 * NQ, kIssuer = kProducer + 1;   // warps behind the softmax warpgroups
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int unit = args.unit, upt = kTileKeys / unit;   // keys of a unit, units of a tile
+    const int ul = args.unit_log2, unit = 1 << ul, upt = kTileKeys >> ul;   // keys of a unit, units of a tile
 
     if (warp == kIssuer) tmem_alloc(&sm.tmem, kTmemCols);
     if (tid == 32 * kProducer) {
         for (int s = 0; s < ST; ++s)
             for (int c = 0; c < kBlocks; ++c) {
-                mbar_init(&sm.full[s][c], 1);
+                mbar_init(&sm.full[s][c], c == 0 ? 2 : 1);   // with the first part come the scales
                 mbar_init(&sm.empty[s][c], 1);
             }
         mbar_init(&sm.s_full[0], 1);
@@ -265,7 +292,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
         return s;
     };
     auto first_tile = [&](int ntiles, int split) { return (int)((int64_t)ntiles * split / args.splits); };
-    // Producer: the copies of tile t, the CTA's n-th, channel block by channel block (one lane per unit).
+    // Producer: the copies of tile t, the CTA's n-th, part by part (one lane per unit), and the keys' scales.
     auto load_tile = [&](int t, int n) -> bool {
         const int st = n % ST;
         const Seg& sg = sm.seg[seg_of(t)];
@@ -275,29 +302,44 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             const int slot = sg.unit(v) * unit, pg = slot / sg.page_size, page = __ldg(sg.table + pg);
             if (page >= 0 && page < sg.n_pages) row = page * sg.page_size + (slot - pg * sg.page_size);
         }
-        const uint32_t live = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0));
+        const int row4 = __shfl_sync(0xFFFFFFFFu, row, (4 * lane) >> ul);   // the unit of keys 4 lane .. 4 lane + 3
+        float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (row4 >= 0) sc = __ldg(reinterpret_cast<const float4*>(sg.scales + row4 + ((4 * lane) & (unit - 1))));
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, row >= 0);
         const int first = sg.pos0 + sg.unit(v) * unit, last = first + unit - 1;
         const bool inside = row >= 0 && last < sg.end && last <= sg.imin && (first >= sg.lmax || (sg.own && last < p.n_sink));
         const int keys = min(kTileKeys, (sg.units - (t - sg.tile0) * upt) * unit);
-        const Tile info = {sg.qa, sg.nq, (keys + 31) / 32, __popc(__ballot_sync(0xFFFFFFFFu, inside)) == upt};
+        const Tile info = {sg.qa, sg.nq, (keys + 31) / 32, __popc(__ballot_sync(0xFFFFFFFFu, inside)) == upt, sg.end,
+                           sg.own ? p.n_sink : 0};
         const CUtensorMap* map = sg.own ? &map_own : &map_prefix;
+        auto put_scales = [&] {
+            *reinterpret_cast<float4*>(&sm.sc[st][4 * lane]) = sc;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.full[st][0]);
+        };
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) {
             bool ok = true;
             if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
             if (c == 0) {
-                if (lane < upt) sm.held[st][lane] = row >= 0;
+                if (lane < upt) sm.upos[st][lane] = row >= 0 ? first : 0x7FFFFF00;
                 if (lane == 0) sm.tile[st] = info;
             }
+            const int upp = 32 >> ul;   // by keys: units of a part
+            const uint32_t bytes = kByKeys ? __popc(live & (((1u << upp) - 1u) << (c * upp))) * unit * kD : __popc(live) * unit * 128;
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], live * unit * (c == 0 ? 128 + 4 : 128));
+            if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], bytes);
             __syncwarp();
             if (row >= 0 && !args.test_starve) {
-                tma_unit(sm.K[st][c] + lane * unit * 128, map, row, c, &sm.full[st][c]);
-                if (c == 0) bulk_load(&sm.sc[st][lane * unit], sg.scales + row, unit * 4, &sm.full[st][0]);
+                if (!kByKeys)
+                    tma_unit(sm.K[st] + c * L::block + lane * unit * 128, map, row, c, &sm.full[st][c]);
+                else if (lane >> (5 - ul) == c)
+                    tma_groups(sm.K[st] + lane * unit * kD, map, row / kGroup, &sm.full[st][c]);
             }
+            if (c == 0 && n >= ST) put_scales();
         }
+        if (n < ST) put_scales();   // the first tiles: the copies go out before the scales are back
         return true;
     };
 
@@ -327,10 +369,10 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             pend = __shfl_sync(0xFFFFFFFFu, pend, 0);
             const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
             if (e > 0) {
-                const int u = (e + unit - 1) / unit;
+                const int u = (e + unit - 1) >> ul;
                 if (lane == 0) sm.seg[n] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
                 ++n;
-                tiles = (u + upt - 1) / upt;
+                tiles = (u + upt - 1) >> (7 - ul);
             }
         }
         int qa = 0;
@@ -351,14 +393,14 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             if (hi > base) {
                 // the sinks' units, then the window's from the first that holds no sink
                 const int ns = min(p.n_sink, hi) - base;
-                const int us = ns > 0 ? (ns + unit - 1) / unit : 0;
-                const int ue = (hi - base + unit - 1) / unit;
-                const int uw = max(us, lo > base ? (lo - base) / unit : 0);
+                const int us = ns > 0 ? (ns + unit - 1) >> ul : 0;
+                const int ue = (hi - base + unit - 1) >> ul;
+                const int uw = max(us, lo > base ? (lo - base) >> ul : 0);
                 const int u = us + max(0, ue - uw);
                 if (u > 0) {
                     if (lane == 0) sm.seg[n] = make_seg(p.own, 1, rb, tiles, u, us, uw - us, qa, c - qa, rend, rmin, rlow);
                     ++n;
-                    tiles += (u + upt - 1) / upt;
+                    tiles += (u + upt - 1) >> (7 - ul);
                 }
             }
             qa = c;
@@ -438,7 +480,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
         // these take, and each stream's waits then leave the other alone.  A tile's products are unrolled.
         const uint32_t lead = elect_one();
         const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const uint32_t k0 = smem_u32(sm.K[0][0]);
+        const uint32_t k0 = smem_u32(sm.K[0]);
         const uint64_t qd = smem_desc(smem_u32(sm.Qs), 16, 1024, kSw128);
         bool ok = true;
         for (int n = 0; n < nt && ok; ++n) {
@@ -447,18 +489,23 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1)) && ok;
             __syncwarp();
             const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
-            const uint64_t a = smem_desc(k0 + st * (kBlocks * kBlockBytes), 16, 1024, kSw128), b = qd + qa * (4096 / 16);
+            const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
             const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+            if (kByKeys) {
+#pragma unroll
+                for (int c = 1; c < kBlocks; ++c) ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
+                __syncwarp();
+            }
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c) {
-                if (c > 0) {
+                if (!kByKeys && c > 0) {
                     ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
                     __syncwarp();
                 }
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    mma_f8(lead, d, a + (c * kBlockBytes + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
+                    mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
             }
             commit(lead, &sm.s_full[n & 1]);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -472,7 +519,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
         // ---- O issuer ----
         const uint32_t lead = elect_one();
         const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
-        const uint32_t k0 = smem_u32(sm.K[0][0]);
+        const uint32_t k0 = smem_u32(sm.K[0]);
         const uint64_t pd = smem_desc(smem_u32(sm.P), 128, 2048, kLayoutNone);
         bool ok = true;
         for (int n = 0; n < nt && ok; ++n) {
@@ -481,31 +528,30 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             __syncwarp();
             const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
             const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
-            const uint64_t a = smem_desc(k0 + st * (kBlocks * kBlockBytes), 16, 1024, kSw128);
+            const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128);
             tc_fence_after();
+            const uint64_t b = pd + qa * (2048 / 16);
+            const uint32_t d = td + kH * qa;
+            // Part i of the tile; its memory is free for a coming tile when its products are done.
+            auto parts = [&](auto product) {
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = kByKeys ? j : i, s = kByKeys ? i : j;
+                        if (s < steps) product(c, a + (c * L::block + s * L::step) / 16, b + s * (512 / 16));
+                    }
+                    commit(lead, &sm.empty[st][i]);
+                }
+            };
             if (kConcat && qn == NQ) {   // the three terms as one product
-#pragma unroll
-                for (int c = 0; c < kBlocks; ++c) {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (s < steps)
-                            mma_f8(lead, td + c * kOCols, a + (c * kBlockBytes + s * 4096) / 16, pd + s * (512 / 16), idesc_pv(3 * R), 1);
-                    commit(lead, &sm.empty[st][c]);   // the block's memory is free for a coming tile
-                }
+                parts([&](int c, uint64_t as, uint64_t bs) { mma_f8(lead, d + c * kOCols, as, bs, idesc_pv(3 * R), 1); });
             } else {
-                const uint64_t b = pd + qa * (2048 / 16);
-                const uint32_t id = idesc_pv(kH * qn), d = td + kH * qa;
+                const uint32_t id = idesc_pv(kH * qn);
+                parts([&](int c, uint64_t as, uint64_t bs) {
 #pragma unroll
-                for (int c = 0; c < kBlocks; ++c) {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (s < steps)
-#pragma unroll
-                            for (int x = 0; x < 3; ++x)
-                                mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), a + (c * kBlockBytes + s * 4096) / 16,
-                                       b + (x * NQ * 2048 + s * 512) / 16, id, 1);
-                    commit(lead, &sm.empty[st][c]);
-                }
+                    for (int x = 0; x < 3; ++x) mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), as, bs + x * NQ * (2048 / 16), id, 1);
+                });
             }
             commit(lead, &sm.pv_done);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -535,7 +581,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
 #pragma unroll
         for (int h = 0; h < kH; ++h) l[h] = 0.0f;
         auto row4 = [&](const float (&a)[R], int j) { return *reinterpret_cast<const float4*>(&a[kH * wg + 4 * j]); };
-        const int ku = key / unit, ko = key % unit;
+        const int ku = key >> ul, ko = key & (unit - 1);
 
         // After a wait that ran out the loop goes on with what is there: every thread passes every barrier.
         for (int n = 0; n < nt; ++n) {
@@ -543,17 +589,13 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
             const Tile tile = sm.tile[st];
             const bool active = wg >= tile.qa && wg < tile.qa + tile.nq;   // this tile's products cover this query
-            bool seen = active, unseen = false;   // by this query; by none of the CTA, within the steps that P K takes
+            bool seen = active;
             if (!tile.interior) {
-                const Seg& sg = sm.seg[seg_of(t0 + n)];
-                const int v = (t0 + n - sg.tile0) * upt + ku, pos = sg.pos0 + sg.unit(v) * unit + ko;
-                const bool stored = v < sg.units && pos < sg.end && sm.held[st][ku], sink = sg.own && pos < p.n_sink;
-                seen = active && stored && pos <= qi && (pos >= qlow || sink);
-                unseen = key < 32 * tile.steps;
-                if (stored)
-                    for (int c = sg.qa; c < sg.qa + sg.nq; ++c) unseen &= !(pos <= sm.qi[c] && (pos >= sm.qlow[c] || sink));
+                const int pos = sm.upos[st][ku] + ko;
+                seen = active && pos < tile.end && pos <= qi && (pos >= qlow || pos < tile.sink);
             }
             const float ts = seen ? sm.sc[st][key] : 0.0f;
+            bool dirty = false;
             wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1));
             tc_fence_after();
             if (active) {
@@ -566,6 +608,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
 #pragma unroll
                     for (int h = 0; h < kH; ++h) z[h] = (__uint_as_float(u[h]) + __uint_as_float(u[16 + h])) * ts;
                 }
+                dirty = !seen && z[0] != z[0];
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.s_free[n & 1]);
@@ -583,12 +626,16 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
                         for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
                     }
                 };
-                relative();
-                float top = x[0];
+                bool move = n == 0;
+                if (n > 0) {
+                    relative();
+                    float top = x[0];
 #pragma unroll
-                for (int h = 1; h < kH; ++h) top = fmaxf(top, x[h]);
+                    for (int h = 1; h < kH; ++h) top = fmaxf(top, x[h]);
+                    move = wg_any(wg, top + lsc > kHeadroom);
+                }
                 // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
-                if (__builtin_expect(wg_any(wg, top + lsc > kHeadroom), 0)) {
+                if (__builtin_expect(move, 0)) {
                     float mx[kH];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -658,12 +705,12 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
                 wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
             }
             if (!active && lane == 0) mbar_arrive(&sm.s_free[n & 1]);
-            if (unseen) {   // S of this tile is done: only P K still reads the row
-#pragma unroll
-                for (int b = wg; b < kBlocks; b += NQ)
+            if (dirty) {   // S of this tile is done: only P K still reads the row
+                for (int b = wg - tile.qa; b < kBlocks; b += tile.nq)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(&sm.K[st][b][key * 128 + 16 * ((j + key) & 7)]) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(&sm.K[st][(key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7)]) =
+                            make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -710,7 +757,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
             fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
         }
         // every copy and product is done: the tiles' memory takes the query's [16][512] bf16
-        uint16_t* ostage = reinterpret_cast<uint16_t*>(&sm.K[0][0][0]) + wg * kH * kD;
+        uint16_t* ostage = reinterpret_cast<uint16_t*>(sm.K[0]) + wg * kH * kD;
         float* po = args.part_o + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + kH * wg) * kD;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
@@ -747,11 +794,13 @@ __global__ void __launch_bounds__(kWg * NQ + 96, (NQ == 1 && ST == 1) ? 2 : 1)
     if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the splits of a block: one CTA per row, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).
+// Joins the splits of a block: one CTA per row, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).  The weights
+// come first, a thread per split, so that the loads of the partial rows do not wait on one another.
 __global__ void __launch_bounds__(128) pages_merge_kernel(const __grid_constant__ KernelArgs args, int NQ) {
     pdl_enter();
+    __shared__ float w[kMaxSplits], red[4], red2[4];
     const PagesAttnParams& p = args.p;
-    const int S = args.splits, R = kH * NQ, tid = threadIdx.x;
+    const int S = args.splits, R = kH * NQ, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int f = blockIdx.x / kH, h = blockIdx.x % kH;
     int blk, c;
     if (p.prefix.B) {
@@ -763,21 +812,43 @@ __global__ void __launch_bounds__(128) pages_merge_kernel(const __grid_constant_
         c = q % NQ;
     }
     const int64_t r0 = ((int64_t)blk * S) * R + 16 * c + h;   // row of split s: r0 + s R
+    const float2* ml = reinterpret_cast<const float2*>(args.part_ml) + r0;
+    const float4* po = reinterpret_cast<const float4*>(args.part_o + r0 * kD) + tid;
+    float2 v[(kMaxSplits + 127) / 128];
     float M = -INFINITY;
-    for (int s = 0; s < S; ++s) M = fmaxf(M, __ldcg(args.part_ml + (r0 + (int64_t)s * R) * 2));
+#pragma unroll
+    for (int i = 0; i < (kMaxSplits + 127) / 128; ++i) {
+        const int s = tid + 128 * i;
+        v[i] = s < S ? __ldcg(ml + (int64_t)s * R) : make_float2(-INFINITY, 0.0f);
+        M = fmaxf(M, v[i].x);
+    }
+    M = redux_max(M);
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     const float Mu = M == -INFINITY ? 0.0f : M;
     float L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (kMaxSplits + 127) / 128; ++i) {
+        const int s = tid + 128 * i;
+        const float e = exp2f(v[i].x - Mu);
+        if (s < S) w[s] = e;
+        L = fmaf(v[i].y, e, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+    if (lane == 0) red2[warp] = L;
+    __syncthreads();
+    L = (red2[0] + red2[1]) + (red2[2] + red2[3]);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
     for (int s = 0; s < S; ++s) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(args.part_ml) + r0 + (int64_t)s * R);
-        if (!(ml.y > 0.0f)) continue;
-        const float w = exp2f(ml.x - Mu);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(args.part_o + (r0 + (int64_t)s * R) * kD) + tid);
-        L = fmaf(ml.y, w, L);
-        o.x = fmaf(v.x, w, o.x);
-        o.y = fmaf(v.y, w, o.y);
-        o.z = fmaf(v.z, w, o.z);
-        o.w = fmaf(v.w, w, o.w);
+        const float4 y = __ldcg(po + (int64_t)s * R * (kD / 4));
+        const float e = w[s];
+        o.x = fmaf(y.x, e, o.x);
+        o.y = fmaf(y.y, e, o.y);
+        o.z = fmaf(y.z, e, o.z);
+        o.w = fmaf(y.w, e, o.w);
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     *reinterpret_cast<uint2*>(p.out + (int64_t)blockIdx.x * kD + 4 * tid) =
@@ -789,18 +860,21 @@ __global__ void __launch_bounds__(128) pages_merge_kernel(const __grid_constant_
 
 struct Plan {
     int nq, blocks, splits;
+    bool two;   // two CTAs on an SM
     size_t o_bytes, bytes;
 };
 
+// Queries of a CTA, and how its keys are split.  Sizes alone decide, so that a workspace can be sized without a device.
 Plan plan(bool prefix, int B, int Q, int64_t keys) {
     Plan pl{};
     const int64_t n = (int64_t)B * Q;
-    const int64_t together = prefix ? n : Q;
-    pl.nq = together >= 3 ? 4 : (int)together;
-    pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
+    const int64_t together = prefix ? n : Q;   // queries that share keys
     int64_t tiles = (keys + kTileKeys - 1) / kTileKeys + (prefix ? 1 : 0);
     if (tiles < 1) tiles = 1;
-    const int64_t ctas = pl.nq == 1 ? 2 * kSplitSMs : kSplitSMs;
+    pl.nq = together >= 3 ? 4 : (int)together;
+    pl.two = pl.nq <= 2;
+    pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
+    const int64_t ctas = pl.two ? 2 * kSplitSMs : kSplitSMs;
     int64_t s = ctas / pl.blocks;
     if (s > tiles) s = tiles;
     if (s < 1) s = 1;
@@ -831,28 +905,36 @@ EncodeFn encoder() {
     return fn;
 }
 
-// The pool as [4 blocks of 128 channels][rows][128 B]: a box is one block of a unit's rows.
-cudaError_t pool_map(const csa2_pages& pg, int unit, CUtensorMap* map) {
+// The pool as a tensor whose boxes land in the tile's order: by channels [4 channel blocks][rows][128 B], a box being
+// one block of a unit's rows; by keys [groups of 8 rows][4 channel blocks][8 rows][128 B], a box being a unit's groups.
+cudaError_t pool_map(const csa2_pages& pg, int unit, bool by_keys, CUtensorMap* map) {
     const EncodeFn fn = encoder();
     if (!fn) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {128, (cuuint64_t)(pg.n_pages * pg.page_size), kBlocks};
-    const cuuint64_t strides[2] = {kD, 128};
-    const cuuint32_t box[3] = {128, (cuuint32_t)unit, 1}, es[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
+    const cuuint64_t rows = (cuuint64_t)(pg.n_pages * pg.page_size);
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    CUresult r;
+    if (by_keys) {
+        const cuuint64_t dims[4] = {128, kGroup, kBlocks, rows / kGroup}, strides[3] = {kD, 128, (cuuint64_t)kGroup * kD};
+        const cuuint32_t box[4] = {128, kGroup, kBlocks, (cuuint32_t)(unit / kGroup)};
+        r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        const cuuint64_t dims[3] = {128, rows, kBlocks}, strides[2] = {kD, 128};
+        const cuuint32_t box[3] = {128, (cuuint32_t)unit, 1};
+        r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NQ, int ST>
+template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas>
 cudaError_t launch(const KernelArgs& a, int blocks, const CUtensorMap& own, const CUtensorMap& prefix, cudaStream_t st) {
     static DeviceOnce attr;
+    const auto kernel = pages_attn_kernel<NQ, ST, kByKeys, kConcat, kCtas>;
     const int smem = (int)sizeof(Smem<NQ, ST>) + 1024;
-    cudaError_t e = attr.run([&] {
-        return cudaFuncSetAttribute(pages_attn_kernel<NQ, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    });
+    cudaError_t e = attr.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
-    return launch_ex(pages_attn_kernel<NQ, ST>, dim3(a.splits, blocks), dim3(kWg * NQ + 96), smem, st, 0, own, prefix, a);
+    return launch_ex(kernel, dim3(a.splits, blocks), dim3(kWg * NQ + 96), smem, st, 0, own, prefix, a);
 }
 
 }  // namespace
@@ -860,29 +942,35 @@ cudaError_t launch(const KernelArgs& a, int blocks, const CUtensorMap& own, cons
 size_t pages_attn_ws_bytes(bool prefix, int B, int Q, int64_t keys) { return plan(prefix, B, Q, keys).bytes; }
 
 cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, cudaStream_t st) {
-    const Plan pl = plan(p.prefix.B != 0, p.B, p.Q, keys);
+    const bool prefix = p.prefix.B != 0;
+    const Plan pl = plan(prefix, p.B, p.Q, keys);
     KernelArgs a{};
     a.p = p;
     a.splits = pl.splits;
     a.test_starve = test_starve_copies();
     a.part_o = (float*)ws;
     a.part_ml = (float*)((char*)ws + pl.o_bytes);
-    // Large boxes cost fewer copies; a window's first unit reaches back over up to unit - 1 keys that no query sees.
-    int unit = p.prefix.B || p.window >= 1024 ? 64 : 32;
-    while (p.own.page_size % unit || (p.prefix.B && p.prefix.page_size % unit)) unit /= 2;
-    a.unit = unit;
-    CUtensorMap own, prefix;
-    cudaError_t e = pool_map(p.own, unit, &own);
+    // A unit lies in one page.  Large ones cost fewer copies; a window's first unit reaches back over up to unit - 1
+    // keys that no query sees.
+    const bool far = prefix || p.window >= 512;
+    auto divides = [&](int u) { return p.own.page_size % u == 0 && (!prefix || p.prefix.page_size % u == 0); };
+    const bool by_keys = !(pl.nq == 4 && far && divides(64));
+    int unit = by_keys ? (far ? 32 : 16) : divides(128) ? 128 : 64;
+    while (!divides(unit)) unit /= 2;
+    while ((1 << a.unit_log2) < unit) ++a.unit_log2;
+    CUtensorMap mo, mp;
+    cudaError_t e = pool_map(p.own, unit, by_keys, &mo);
     if (e != cudaSuccess) return e;
-    if (p.prefix.B) {
-        e = pool_map(p.prefix, unit, &prefix);
+    if (prefix) {
+        e = pool_map(p.prefix, unit, by_keys, &mp);
         if (e != cudaSuccess) return e;
     } else {
-        prefix = own;
+        mp = mo;
     }
-    e = pl.nq == 1   ? launch<1, 1>(a, pl.blocks, own, prefix, st)
-        : pl.nq == 2 ? launch<2, 2>(a, pl.blocks, own, prefix, st)
-                     : launch<4, 2>(a, pl.blocks, own, prefix, st);
+    e = pl.nq == 1   ? launch<1, 1, true, true, 2>(a, pl.blocks, mo, mp, st)
+        : pl.nq == 2 ? launch<2, 1, true, false, 2>(a, pl.blocks, mo, mp, st)
+        : by_keys    ? launch<4, 2, true, false, 1>(a, pl.blocks, mo, mp, st)
+                     : launch<4, 2, false, false, 1>(a, pl.blocks, mo, mp, st);
     if (e != cudaSuccess || pl.splits == 1) return e;
     return launch_ex(pages_merge_kernel, dim3((unsigned)(p.B * p.Q * kH)), dim3(128), 0, st, 0, a, pl.nq);
 }
