@@ -291,7 +291,10 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
         while (s + 1 < sm.nseg && tile >= sm.seg[s + 1].tile0) ++s;
         return s;
     };
-    auto first_tile = [&](int ntiles, int split) { return (int)((int64_t)ntiles * split / args.splits); };
+    auto first_tile = [&](int ntiles, int split) {   // the first ntiles % splits CTAs take one tile more
+        const int q = ntiles / args.splits, r = ntiles - q * args.splits;
+        return split * q + min(split, r);
+    };
     // Producer: the copies of tile t, the CTA's n-th, part by part (one lane per unit), and the keys' scales.
     auto load_tile = [&](int t, int n) -> bool {
         const int st = n % ST;
@@ -358,52 +361,60 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             sm.qi[lane] = i;
             sm.qlow[lane] = low;
         }
-        int n = 0, tiles = 0, imax = -1, imin = 0x7FFFFFFF;
+        // Each lane's run of queries of one sequence: its extent and what its keys range over (every lane < nq alike).
+        const bool mine = lane < nq;
+        const int seq = mine ? b : -1;
+        int count = 0, head = 1, hi = 0, lo = 0x7FFFFFFF, rmin = 0x7FFFFFFF, rlow = 0, imax = -1, imin = 0x7FFFFFFF;
 #pragma unroll
         for (int c = 0; c < NQ; ++c) {
-            const int ic = __shfl_sync(0xFFFFFFFFu, i, c);
-            imax = max(imax, ic);
-            if (c < nq) imin = min(imin, ic);
+            const int oi = __shfl_sync(0xFFFFFFFFu, i, c), ol = __shfl_sync(0xFFFFFFFFu, low, c);
+            const bool same = __shfl_sync(0xFFFFFFFFu, seq, c) == seq;
+            if (c < nq) {
+                imax = max(imax, oi);
+                imin = min(imin, oi);
+            }
+            if (c < nq && same) {
+                ++count;
+                if (c < lane) head = 0;
+                rmin = min(rmin, oi);
+                rlow = max(rlow, ol);
+                if (oi >= 0) {
+                    hi = max(hi, oi < end ? oi + 1 : end);
+                    lo = min(lo, ol);
+                }
+            }
         }
+        int n = 0, tiles = 0;
         if (shared_prefix) {
             pend = __shfl_sync(0xFFFFFFFFu, pend, 0);
             const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
             if (e > 0) {
                 const int u = (e + unit - 1) >> ul;
-                if (lane == 0) sm.seg[n] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
-                ++n;
+                if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
+                n = 1;
                 tiles = (u + upt - 1) >> (7 - ul);
             }
         }
-        int qa = 0;
-        while (qa < nq) {   // runs of queries of one sequence
-            const int rb = __shfl_sync(0xFFFFFFFFu, b, qa), rend = __shfl_sync(0xFFFFFFFFu, end, qa);
-            int c = qa, hi = 0, lo = 0x7FFFFFFF, rmin = 0x7FFFFFFF, rlow = 0;
-            while (c < nq && __shfl_sync(0xFFFFFFFFu, b, c) == rb) {
-                const int ic = __shfl_sync(0xFFFFFFFFu, i, c), lc = __shfl_sync(0xFFFFFFFFu, low, c);
-                rmin = min(rmin, ic);
-                rlow = max(rlow, lc);
-                if (ic >= 0) {
-                    hi = max(hi, ic < rend ? ic + 1 : rend);
-                    lo = min(lo, lc);
+        {
+            // the sinks' units, then the window's from the first that holds no sink
+            const int base = p.own.pos0, ns = min(p.n_sink, hi) - base;
+            const int us = ns > 0 ? (ns + unit - 1) >> ul : 0;
+            const int ue = (hi - base + unit - 1) >> ul;
+            const int uw = max(us, lo > base ? (lo - base) >> ul : 0);
+            const int u = mine && head && hi > base ? us + max(0, ue - uw) : 0;
+            const int mytiles = (u + upt - 1) >> (7 - ul);
+            int at = n, tile0 = tiles;   // lists and tiles of the runs before this one
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+                const int ot = __shfl_sync(0xFFFFFFFFu, mytiles, c);
+                if (c < lane) {
+                    at += ot > 0;
+                    tile0 += ot;
                 }
-                ++c;
+                n += ot > 0;
+                tiles += ot;
             }
-            const int base = p.own.pos0;
-            if (hi > base) {
-                // the sinks' units, then the window's from the first that holds no sink
-                const int ns = min(p.n_sink, hi) - base;
-                const int us = ns > 0 ? (ns + unit - 1) >> ul : 0;
-                const int ue = (hi - base + unit - 1) >> ul;
-                const int uw = max(us, lo > base ? (lo - base) >> ul : 0);
-                const int u = us + max(0, ue - uw);
-                if (u > 0) {
-                    if (lane == 0) sm.seg[n] = make_seg(p.own, 1, rb, tiles, u, us, uw - us, qa, c - qa, rend, rmin, rlow);
-                    ++n;
-                    tiles += (u + upt - 1) >> (7 - ul);
-                }
-            }
-            qa = c;
+            if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow);
         }
         if (lane == 0) {
             sm.nseg = n;
@@ -423,11 +434,15 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                 v[k][1] = __ldg(src + 1);
             }
         }
+        float top[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = redux_max(top[k]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int r = warp + 4 * NQ * k, c = r >> 4, h = r & 15;
-            const float mx = redux_max(fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1])));
-            const int e = max((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127 - 7, -120);
+            const int e = max((int)((__float_as_uint(top[k]) >> 23) & 0xFFu) - 127 - 7, -120);
             const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -738,12 +753,12 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
         wg_bar(wg);
         if (key < kH) {
             const int r = kH * wg + key;
-            const float sum = (sm.wmax[0][r] + sm.wmax[1][r]) + (sm.wmax[2][r] + sm.wmax[3][r]), m = sm.mref[r];
+            const float sum = (sm.wmax[0][r] + sm.wmax[1][r]) + (sm.wmax[2][r] + sm.wmax[3][r]), ref = sm.mref[r];
             if (args.splits > 1) {
                 float* ml = args.part_ml + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + r) * 2;
-                *reinterpret_cast<float2*>(ml) = make_float2(m, sum);
+                *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
             } else if (p.lse && wg < nq) {
-                p.lse[(int64_t)(f0 + wg) * kH + key] = sum > 0.0f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                p.lse[(int64_t)(f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
             }
             sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
         }
@@ -756,37 +771,34 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             const float4 f = row4(sm.fac, j);
             fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
         }
-        // every copy and product is done: the tiles' memory takes the query's [16][512] bf16
-        uint16_t* ostage = reinterpret_cast<uint16_t*>(sm.K[0]) + wg * kH * kD;
         float* po = args.part_o + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + kH * wg) * kD;
+        // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
+        uint16_t* out = p.out + ((int64_t)(f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            const int dim = 128 * b + key;
             uint32_t o[kTerms][16];
 #pragma unroll
             for (int y = 0; y < kTerms; ++y) tmem_ld_32x32b_x16(ocol(b, y), o[y]);
             tmem_ld_wait();
+            float y[kH];
 #pragma unroll
             for (int h = 0; h < kH; ++h) {
-                float y = __uint_as_float(o[0][h]);
+                y[h] = __uint_as_float(o[0][h]);
 #pragma unroll
-                for (int x = 1; x < kTerms; ++x) y += __uint_as_float(o[x][h]);
-                y *= fac[h];
-                if (args.splits > 1) {
-                    po[h * kD + dim] = y;
-                } else {
-                    const __nv_bfloat16 yb = __float2bfloat16_rn(y);
-                    ostage[h * kD + dim] = *reinterpret_cast<const uint16_t*>(&yb);
+                for (int x = 1; x < kTerms; ++x) y[h] += __uint_as_float(o[x][h]);
+                y[h] *= fac[h];
+            }
+            if (args.splits > 1) {
+#pragma unroll
+                for (int h = 0; h < kH; ++h) po[h * kD + 128 * b + key] = y[h];
+            } else if (wg < nq) {
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const uint32_t own = pack_bf16(y[h], y[h + 8]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                    *reinterpret_cast<uint32_t*>(out + h * kD + 128 * b) =
+                        (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
                 }
             }
-        }
-        if (args.splits == 1) {
-            wg_bar(wg);
-            const uint4* src = reinterpret_cast<const uint4*>(ostage);
-            uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)(f0 + wg) * kH * kD);
-            if (wg < nq)
-#pragma unroll
-                for (int j = 0; j < kH * kD / 8 / kWg; ++j) dst[key + kWg * j] = src[key + kWg * j];
         }
         tc_fence_before();
     }
