@@ -455,9 +455,15 @@ def csa2_layer_step(mode, kv, q_pos, q, swa, swa_sc, swa_pos0, idx, k=TOPK, iq=N
 
 
 # ---- the paged FP8 cache -----------------------------------------------------------------------
+# These calls serve decode steps whose kernels take a few microseconds, so the binding spends as little:
+# plain integers for pointers, the raw stream, sizes looked up once.
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
 
 def _on(t, dtype, numel, name, dev):
-    """A contiguous tensor of this dtype and size on the current device (number dev)."""
+    """Address of a contiguous tensor of this dtype and size on the current device (number dev)."""
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of {dtype} on cuda:{dev}, the current device, got "
                          f"{t.dtype} on {t.device} with strides {t.stride()}")
@@ -503,6 +509,7 @@ class Pages:
             _on(t, dt, n, name, self.device)
         self._t = (kv, kv_sc, table, n_tokens)
         self.n_pages, self.page_size, self.B, self.max_pages, self.pos0 = n_pages, ps, B, width, pos0
+        self.cap = width * ps   # tokens that the table can name for a sequence
         self._c = csa2_pages(kv.data_ptr(), kv_sc.data_ptr(), table.data_ptr(), n_tokens.data_ptr(), n_pages, ps, B,
                              width, pos0)
 
@@ -510,11 +517,6 @@ class Pages:
     kv_sc = property(lambda self: self._t[1])
     table = property(lambda self: self._t[2])
     n_tokens = property(lambda self: self._t[3])
-
-    @property
-    def cap(self):
-        """Tokens that the table can name for a sequence."""
-        return self.max_pages * self.page_size
 
     def c(self, dev):
         if self.device != dev:
@@ -526,20 +528,22 @@ _flags = {}
 
 
 def _flag(dev):
-    """This device's sticky error flag of the paged attentions (kept for the life of the process, so
-    that captured graphs can name it)."""
-    if dev not in _flags:
+    """Address of this device's sticky error flag of the paged attentions (kept for the life of the
+    process, so that captured graphs can name it)."""
+    f = _flags.get(dev)
+    if f is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("make one paged attention call on this device before capturing one into a graph")
-        _flags[dev] = torch.zeros(1, dtype=torch.int32, device=f"cuda:{dev}")
+        t = torch.zeros(64, dtype=torch.int32, device=f"cuda:{dev}")
         torch.cuda.current_stream().synchronize()   # other streams may use it next
-    return _flags[dev]
+        f = _flags[dev] = (t.data_ptr(), t)
+    return f[0]
 
 
 def csa2_flag_status(clear=False):
     """Waits for the current stream; raises CSA2Error (CSA2_ERR_TIMEOUT) if a paged attention call on
     the current device had a device-side wait run out of time (its results are not valid)."""
-    _check(lib().csa2_flag_status(_ptr(_flag(torch.cuda.current_device())), 1 if clear else 0, _stream()))
+    _check(lib().csa2_flag_status(_flag(torch.cuda.current_device()), 1 if clear else 0, _stream()))
 
 
 def csa2_pages_append(x, pages, seq, pos, inv_freq=None, norm_w=None, eps=1e-6, normalise=True):
@@ -547,39 +551,59 @@ def csa2_pages_append(x, pages, seq, pos, inv_freq=None, norm_w=None, eps=1e-6, 
     (seq i32 [rows], pos i32 [rows]); rows with seq < 0 or no page are dropped.  inv_freq f32 [32],
     norm_w f32 [512] or None.  The caller updates pages.n_tokens."""
     dev = torch.cuda.current_device()
-    if x.dtype is not torch.bfloat16 or x.get_device() != dev or x.dim() != 2 or x.shape[1] != D or x.stride(1) != 1:
-        raise ValueError(f"x: expected bf16 rows [rows, {D}] on cuda:{dev}, got {x.dtype} {tuple(x.shape)} on {x.device} "
-                         f"with strides {x.stride()}")
-    rows = x.shape[0]
-    stride = x.stride(0) if rows > 1 else D
-    _check(lib().csa2_pages_append(
-        x.data_ptr(), stride, rows, _on(seq, torch.int32, rows, "seq", dev), _on(pos, torch.int32, rows, "pos", dev),
+    shape, stride = x.shape, x.stride()
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev or len(shape) != 2 or shape[1] != D or stride[1] != 1:
+        raise ValueError(f"x: expected bf16 rows [rows, {D}] on cuda:{dev}, got {x.dtype} {tuple(shape)} on {x.device} "
+                         f"with strides {stride}")
+    rows = shape[0]
+    st = lib().csa2_pages_append(
+        x.data_ptr(), stride[0] if rows > 1 else D, rows, _on(seq, torch.int32, rows, "seq", dev),
+        _on(pos, torch.int32, rows, "pos", dev),
         None if inv_freq is None else _on(inv_freq, torch.float32, 32, "inv_freq", dev),
         None if norm_w is None else _on(norm_w, torch.float32, D, "norm_w", dev), eps, 1 if normalise else 0,
-        pages.c(dev), torch.cuda.current_stream().cuda_stream))
+        pages.c(dev), _raw_stream(dev))
+    if st:
+        _check(st)
 
 
-def _pages_attn_outputs(q, q_pos, pages, out, lse, dev):
-    if q_pos.dim() != 2 or q_pos.shape[0] != pages.B:
-        raise ValueError(f"q_pos: expected [{pages.B}, Q], got {tuple(q_pos.shape)}")
-    n = q_pos.numel()
+_ws_bytes = {}
+
+
+def _pages_attn_args(op, q, q_pos, pages, keys, out, lse, ws, dev):
+    """Outputs and addresses of a paged attention call: (out, lse, Q, q, q_pos, out, lse, ws, its bytes).
+
+    Without a caller's workspace the call gets one of its own: torch's allocator orders its reuse by
+    stream, and a captured call keeps its in the graph's pool.  A call whose keys are not split needs none."""
+    shape = q_pos.shape
+    if len(shape) != 2 or shape[0] != pages.B:
+        raise ValueError(f"q_pos: expected [{pages.B}, Q], got {tuple(shape)}")
+    B, Q = shape
+    n = B * Q
+    qp, pp = _on(q, torch.bfloat16, n * H * D, "q", dev), _on(q_pos, torch.int32, n, "q_pos", dev)
     if out is None:
-        out = torch.empty((*q_pos.shape, H, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q) if q.shape == (B, Q, H, D) else q.new_empty((B, Q, H, D))
+        op_ = out.data_ptr()
+    else:
+        op_ = _on(out, torch.bfloat16, n * H * D, "out", dev)
+    lp = None
     if lse is True:
-        lse = torch.empty((*q_pos.shape, H), dtype=torch.float32, device=q.device)
-    elif lse is False:
+        lse = q.new_empty((B, Q, H), dtype=torch.float32)
+        lp = lse.data_ptr()
+    elif lse is False or lse is None:
         lse = None
-    return (out, lse, _on(q, torch.bfloat16, n * H * D, "q", dev), _on(q_pos, torch.int32, n, "q_pos", dev),
-            _on(out, torch.bfloat16, n * H * D, "out", dev),
-            None if lse is None else _on(lse, torch.float32, n * H, "lse", dev))
-
-
-def _scratch(op, pages, Q, keys, ws, device):
-    """A workspace of this call's own (torch's allocator orders its reuse by stream, and a captured call
-    keeps its in the graph's pool), or the caller's."""
-    if ws is None:
-        ws = torch.empty(lib().csa2_workspace_bytes(op, pages.B, Q, keys, 0, 0), dtype=torch.uint8, device=device)
-    return ws
+    else:
+        lp = _on(lse, torch.float32, n * H, "lse", dev)
+    if ws is not None:
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: expected a contiguous tensor on cuda:{dev}, got one on {ws.device}")
+        return out, lse, Q, qp, pp, op_, lp, ws.data_ptr(), ws.numel() * ws.element_size()
+    key = (op, B, Q, keys)
+    nbytes = _ws_bytes.get(key)
+    if nbytes is None:
+        nbytes = _ws_bytes[key] = lib().csa2_workspace_bytes(op, B, Q, keys, 0, 0)
+    if nbytes <= 256:   # nothing is split: the call does not touch it
+        return out, lse, Q, qp, pp, op_, lp, _flag(dev), nbytes
+    return out, lse, Q, qp, pp, op_, lp, q.new_empty((nbytes,), dtype=torch.uint8).data_ptr(), nbytes
 
 
 def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None, sm_scale=1.0 / math.sqrt(D),
@@ -587,13 +611,13 @@ def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None
     """Sliding-window attention over a paged cache; tokens at positions below n_sink stay visible.
     q bf16 [B,Q,16,512], q_pos i32 [B,Q] (negative = no query) -> out bf16 [B,Q,16,512] (, lse f32 [B,Q,16])."""
     dev = torch.cuda.current_device()
-    pg = pages.c(dev)
-    out, lse, qp, pp, op, lp = _pages_attn_outputs(q, q_pos, pages, out, lse, dev)
+    pg, flag = pages.c(dev), _flag(dev)
+    out, lse, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_WINDOW_ATTN, q, q_pos, pages, min(window + n_sink, pages.cap),
+                                                           out, lse, ws, dev)
     rp = None if replay_start is None else _on(replay_start, torch.int32, pages.B, "replay_start", dev)
-    Q = q_pos.shape[1]
-    ws = _scratch(OP_WINDOW_ATTN, pages, Q, min(window + n_sink, pages.cap), ws, q.device)
-    _check(lib().csa2_window_attn(qp, pg, pp, Q, window, n_sink, rp, sm_scale, op, lp, ws.data_ptr(),
-                                  ws.numel(), _flag(dev).data_ptr(), torch.cuda.current_stream().cuda_stream))
+    st = lib().csa2_window_attn(qp, pg, pp, Q, window, n_sink, rp, sm_scale, op, lp, wp, wn, flag, _raw_stream(dev))
+    if st:
+        _check(st)
     return out if lse is None else (out, lse)
 
 
@@ -601,10 +625,10 @@ def csa2_prefix_attn(q, prefix, pages, q_pos, sm_scale=1.0 / math.sqrt(D), out=N
     """Attention of a batch over a shared prefix (Pages of one table row) and each sequence's own pages,
     under one causal softmax.  q bf16 [B,Q,16,512], q_pos i32 [B,Q] -> out bf16 (, lse f32 [B,Q,16])."""
     dev = torch.cuda.current_device()
-    pf, pg = prefix.c(dev), pages.c(dev)
-    out, lse, qp, pp, op, lp = _pages_attn_outputs(q, q_pos, pages, out, lse, dev)
-    Q = q_pos.shape[1]
-    ws = _scratch(OP_PREFIX_ATTN, pages, Q, prefix.cap + pages.cap, ws, q.device)
-    _check(lib().csa2_prefix_attn(qp, pf, pg, pp, Q, sm_scale, op, lp, ws.data_ptr(), ws.numel(),
-                                  _flag(dev).data_ptr(), torch.cuda.current_stream().cuda_stream))
+    pf, pg, flag = prefix.c(dev), pages.c(dev), _flag(dev)
+    out, lse, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_PREFIX_ATTN, q, q_pos, pages, prefix.cap + pages.cap, out, lse,
+                                                           ws, dev)
+    st = lib().csa2_prefix_attn(qp, pf, pg, pp, Q, sm_scale, op, lp, wp, wn, flag, _raw_stream(dev))
+    if st:
+        _check(st)
     return out if lse is None else (out, lse)

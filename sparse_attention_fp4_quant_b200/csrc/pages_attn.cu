@@ -12,8 +12,8 @@
 //       elements 2^-10 below the row's largest (each row scaled by its own power of two),
 //       which are held to 2^-18 of it.  hi and lo are separate columns of S, added in fp32.
 //   P   each weight times its token scale, as f16 with 2^12 of headroom below the maximum,
-//       split in three E5M2 terms (f16's exponent range): at least 9 significant bits and
-//       nothing lost down to 2^-36 of the largest weight.
+//       split in three E5M2 terms (f16's exponent range): at least 9 significant bits; what is
+//       smaller than 2^-26 of the row's largest is held to 2^-29 of it (E5M2's smallest step).
 // Softmax: fp32, one thread per key, one pass with a running reference m per row.  The
 // reference is the maximum of z + log2(token scale), the size of what enters P, and it moves
 // only when a tile exceeds it by 2^3 (P keeps that much room), so the accumulators are
@@ -888,7 +888,7 @@ Plan plan(bool prefix, int B, int Q, int64_t keys) {
     pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
     const int64_t ctas = pl.two ? 2 * kSplitSMs : kSplitSMs;
     int64_t s = ctas / pl.blocks;
-    if (s > tiles) s = tiles;
+    if (s > tiles / 2) s = tiles / 2;   // two tiles at least: a third costs a CTA less than the join does
     if (s < 1) s = 1;
     pl.splits = (int)s;
     pl.bytes = 256;
@@ -973,11 +973,10 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
     CUtensorMap mo, mp;
     cudaError_t e = pool_map(p.own, unit, by_keys, &mo);
     if (e != cudaSuccess) return e;
-    if (prefix) {
+    mp = mo;
+    if (prefix && (p.prefix.kv != p.own.kv || p.prefix.n_pages * p.prefix.page_size != p.own.n_pages * p.own.page_size)) {
         e = pool_map(p.prefix, unit, by_keys, &mp);
         if (e != cudaSuccess) return e;
-    } else {
-        mp = mo;
     }
     e = pl.nq == 1   ? launch<1, 1, true, true, 2>(a, pl.blocks, mo, mp, st)
         : pl.nq == 2 ? launch<2, 1, true, false, 2>(a, pl.blocks, mo, mp, st)

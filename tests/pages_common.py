@@ -76,12 +76,17 @@ def attend(q, parts, scale):
     The bound counts, in relative terms of the value it stands on: the output's bf16 rounding 2^-8;
     each probability's rounding 2^-9 (three E5M2 terms, or one f16); and the logits: the query held
     to 2^-18 of the head's largest value, products summed in fp32 with at most 2^-18 of the sum of
-    their magnitudes, an error dz that changes a weight by at most 2 dz; the exponential 2^-20."""
+    their magnitudes, an error dz that changes a weight by at most 2 dz; the exponential 2^-20.
+
+    One absolute term beside them: a weight enters the product times its token's scale, with the row's
+    largest such value at 2^12 or above, and E5M2's step is never finer than 2^-16, so the last term's
+    rounding (half a step) is up to 2^-17 / 2^12 = 2^-29 of the largest, times the key's E4M3 code."""
     keys = [cache.kv[cache.row(b, j)] for cache, b, pos in parts for j in pos]
     if not keys:
         return np.zeros((H, D)), np.full(H, -np.inf), np.zeros((H, D)), np.zeros(H)
     sc = np.array([cache.kv_sc[cache.row(b, j)] for cache, b, pos in parts for j in pos], np.float64)
-    k = E4M3[np.array(keys)] * sc[:, None]
+    codes = E4M3[np.array(keys)]
+    k = codes * sc[:, None]
     z = q @ k.T * scale
     m = z.max(1, keepdims=True)
     p = np.exp(z - m)
@@ -91,6 +96,7 @@ def attend(q, parts, scale):
     dz = scale * 2.0 ** -18 * (np.abs(q).max(1)[:, None] * np.abs(k).sum(1) + np.abs(q) @ np.abs(k).T)
     mean_dz = (w * dz).sum(1)
     tol = 2.0 ** -8 * np.abs(out) + (w * (2.0 ** -9 + 2.0 ** -20 + 2 * dz)) @ np.abs(k) + (2 * mean_dz)[:, None] * np.abs(out)
+    tol = tol + 2.0 ** -29 * (w * sc).max(1)[:, None] * np.abs(codes).sum(0)
     return out, lse, tol + 1e-30, mean_dz + dz.max(1) * 2.0 ** -8 + 2.0 ** -20 * (1 + np.abs(lse))
 
 

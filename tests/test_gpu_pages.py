@@ -201,6 +201,26 @@ def test_weight_behind_one_dominant_key(csa):
     check(out, lse, reference(q, np.array([[n - 1]], np.int32), [(cache, True)], None, 0))
 
 
+@pytest.mark.parametrize("n,Q", [(30001, 1), (20000, 5)])
+def test_weight_behind_a_first_token(csa, n, Q):
+    """The same with scales as a normalised latent has them: the first token's weight comes from the query's direction."""
+    cache = Cache(3, [n], 64)
+    for j in range(n):
+        at = cache.row(0, j)
+        cache.kv[at][0] = 0
+        cache.kv_sc[at] = 0.01
+    at = cache.row(0, 0)
+    cache.kv[at] = 0
+    cache.kv[at][0] = 0x7E   # 448
+    cache.kv_sc[at] = 0.0163
+    q = torch.zeros((1, Q, H, D))
+    q[..., 0] = math.log(n) * math.sqrt(D) / (448 * 0.0163)
+    q_pos = np.arange(n - Q, n, dtype=np.int32)[None]
+    q = q.to(torch.bfloat16)
+    out, lse = run_window(csa, cache, q, q_pos, 1 << 30, 0)
+    check(out, lse, reference(q, q_pos, [(cache, True)], None, 0))
+
+
 # ---- shared prefix -----------------------------------------------------------------------------
 
 def run_prefix(csa, prefix, own, q, q_pos, **kw):
