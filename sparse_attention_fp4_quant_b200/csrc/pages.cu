@@ -2,11 +2,11 @@
 // position, and the E4M3 row with its token scale, in one pass over the row.
 //
 // A warp takes a row at a time and fetches the next one meanwhile.  Lane l holds channels
-// 8 l .. 8 l + 7 and 256 + 8 l .. (two 16-byte loads, two 8-byte code stores), so the rotated
-// channels 448 .. 511 lie in lanes 24 .. 31; lane k computes the angle of pair k (one each), and
-// the eight lanes fetch the four pairs they rotate by shuffles.  The angle pos * inv_freq is
-// formed in fp64 and reduced to a fraction of a turn before the fp32 sine: at position 10^6 an
-// fp32 product would be off by up to 0.03 radian.
+// 8 l .. 8 l + 7, for l < 24 also 256 + 8 l .., and the pair 448 + 2 l, 449 + 2 l: one rotated
+// pair in every lane, each with its own angle.  The kernel is bound by instructions (430 a row
+// in its first form, 20.8 us for 32,768 rows), and this split takes the fewest.  The angle
+// pos * inv_freq is formed in fp64 and reduced to a fraction of a turn before the fp32 sine: at
+// position 10^6 an fp32 product would be off by up to 0.03 radian.
 // The norm's factor 1 / rms is common to a row, so the codes do not depend on it: it is applied
 // to the scale alone.  With a = amax |x w| (rotated), code = E4M3(x w * (448 / a)) and
 // scale = a / 448 / rms; the quotient is within 2^-22 of the definition's, so a code differs
@@ -33,6 +33,12 @@ __device__ __forceinline__ float warp_max(float v) {
     return r;
 }
 
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Four floats -> four E4M3 bytes (nearest, ties to even, saturating).
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
@@ -44,6 +50,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // A row on its way in: its bytes and where it goes.
 struct Row {
     uint4 raw[2];
+    uint32_t pair;
     int seq, pos;
 };
 
@@ -59,7 +66,8 @@ __global__ void __launch_bounds__(32 * kPW, kPCtas) pages_append_kernel(const ui
     auto fetch = [&](int64_t i, Row& d) {
         const uint4* src = reinterpret_cast<const uint4*>(x + i * x_stride);
         d.raw[0] = __ldg(src + lane);
-        d.raw[1] = __ldg(src + 32 + lane);
+        d.raw[1] = lane < 24 ? __ldg(src + 32 + lane) : make_uint4(0, 0, 0, 0);
+        d.pair = __ldg(reinterpret_cast<const uint32_t*>(src) + 224 + lane);
         d.seq = __ldg(seq + i);
         d.pos = __ldg(pos + i);
     };
@@ -85,13 +93,16 @@ __global__ void __launch_bounds__(32 * kPW, kPCtas) pages_append_kernel(const ui
     };
     Row cur, next;
     fetch(r, cur);
-    float w[16];
+    float w[18];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // channels 8 lane .. + 7 and 256 + 8 lane .. + 7
-        const float4 v = norm_w ? __ldg(reinterpret_cast<const float4*>(norm_w) + 64 * (j >> 1) + 2 * lane + (j & 1))
-                                : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    for (int j = 0; j < 4; ++j) {
+        const bool have = norm_w && (j < 2 || lane < 24);
+        const float4 v = have ? __ldg(reinterpret_cast<const float4*>(norm_w) + 64 * (j >> 1) + 2 * lane + (j & 1))
+                              : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
         w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
     }
+    w[16] = norm_w ? __ldg(norm_w + 448 + 2 * lane) : 1.0f;
+    w[17] = norm_w ? __ldg(norm_w + 449 + 2 * lane) : 1.0f;
     const double freq = inv_freq ? (double)__ldg(inv_freq + lane) * 0.15915494309189533577 : 0.0;   // turns per position
     int slot = slot_of(cur);
     int page = page_of(cur, slot);
@@ -105,7 +116,7 @@ __global__ void __launch_bounds__(32 * kPW, kPCtas) pages_append_kernel(const ui
             row = (int64_t)page * pg.page_size + at;
         }
         if (row >= 0) {
-            float v[16];
+            float v[18];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint32_t u[4] = {cur.raw[j].x, cur.raw[j].y, cur.raw[j].z, cur.raw[j].w};
@@ -115,52 +126,50 @@ __global__ void __launch_bounds__(32 * kPW, kPCtas) pages_append_kernel(const ui
                     v[8 * j + 2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
                 }
             }
+            v[16] = __uint_as_float(cur.pair << 16);
+            v[17] = __uint_as_float(cur.pair & 0xFFFF0000u);
             float rn = 1.0f;
             if (normalise) {
                 float ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ss = fmaf(v[i], v[i], ss);
-                rn = 1.0f / sqrtf(warp_sum(ss) * (1.0f / kD) + eps);
+                for (int i = 0; i < 18; ++i) ss = fmaf(v[i], v[i], ss);
+                rn = rsqrtf(warp_sum(ss) * (1.0f / kD) + eps);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= w[i];
+            for (int i = 0; i < 18; ++i) v[i] *= w[i];
             if (inv_freq) {
                 const double turns = (double)cur.pos * freq;
                 float sn, cs;   // of at most half a turn: the fast functions are within 2^-20 there
                 __sincosf((float)((turns - rint(turns)) * 6.283185307179586477), &sn, &cs);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = (4 * (lane - 24) + i) & 31;
-                    const float c = __shfl_sync(0xFFFFFFFFu, cs, k), sv = __shfl_sync(0xFFFFFFFFu, sn, k);
-                    if (lane >= 24) {
-                        const float a = v[8 + 2 * i], b = v[9 + 2 * i];
-                        v[8 + 2 * i] = a * c - b * sv;
-                        v[9 + 2 * i] = a * sv + b * c;
-                    }
-                }
+                const float a = v[16], b = v[17];
+                v[16] = a * cs - b * sn;
+                v[17] = a * sn + b * cs;
             }
             float mx = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(v[i]));
+            for (int i = 0; i < 18; ++i) mx = fmaxf(mx, fabsf(v[i]));
             mx = warp_max(mx);
-            float up = 1.0f;
+            float down = 1.0f;
             if (mx < 1e-30f) {   // 448 / mx would overflow: work on 2^80 times the row
-                up = 1.2089258196146292e24f;
-                mx *= up;
+                mx *= 1.2089258196146292e24f;
+                down = 8.271806125530277e-25f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= up;
+                for (int i = 0; i < 18; ++i) v[i] *= 1.2089258196146292e24f;
             }
-            const float inv = mx > 0.0f ? 448.0f / mx : 0.0f;
+            const float a448 = mx * (1.0f / 448.0f);   // in [2^-108, 2^120]: its approximate reciprocal is within 1 ulp
+            const float inv = mx > 0.0f ? rcp(a448) : 0.0f;
             uint8_t* dst = pg.kv + row * kD;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = v[8 * j + i] * inv;
-                *reinterpret_cast<uint2*>(dst + 256 * j + 8 * lane) =
-                    make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+                if (j == 0 || lane < 24)
+                    *reinterpret_cast<uint2*>(dst + 256 * j + 8 * lane) =
+                        make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
             }
-            if (lane == 0) pg.kv_sc[row] = mx / 448.0f * rn * (1.0f / up);
+            *reinterpret_cast<uint16_t*>(dst + 448 + 2 * lane) = (uint16_t)e4m3x4(v[16] * inv, v[17] * inv, 0.0f, 0.0f);
+            if (lane == 0) pg.kv_sc[row] = a448 * rn * down;
         }
         if (!more) break;
         r += step;
