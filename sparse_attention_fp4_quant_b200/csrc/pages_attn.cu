@@ -35,6 +35,7 @@ constexpr int kTileKeys = 128;
 constexpr int kGroup = 8;                              // keys of one swizzle atom
 constexpr int kBlocks = kD / 128;                      // channel blocks of 128 channels: 128 bytes, a swizzle row
 constexpr int kTileBytes = kTileKeys * kD;             // 64 KB
+constexpr int kAux = 128;                              // producer, S issuer, O issuer and an idle warp: the oldest, which issue first
 constexpr int kWg = 128;                               // threads of a softmax warpgroup: one query, a thread per key
 constexpr float kHeadroom = 3.0f;                      // log2 of how far a weight may exceed the reference
 constexpr float kPScale = 4096.0f;                     // weight 1 at 2^12, 2^15 with the headroom: below f16's and E5M2's largest
@@ -88,6 +89,15 @@ struct Layout {
     static constexpr uint32_t step = 4 * group;                   // 32 keys
 };
 
+// A CTA's item (queries and a split of their keys): what the producer tells the other roles.
+template <int NQ>
+struct Item {
+    int f0, nq;     // first query (b Q + q) and count
+    int tiles;
+    int64_t part;   // block * splits + split
+    int qi[NQ], qlow[NQ];   // each query's token, and the first that its window holds
+};
+
 template <int NQ, int ST>
 struct Smem {
     static constexpr int R = kH * NQ;
@@ -101,12 +111,13 @@ struct Smem {
     alignas(16) float mref[R];
     alignas(16) float fac[R];
     alignas(16) float rowf[R];
-    Seg seg[NQ + 1];
-    int nseg, ntiles;
-    int qi[NQ], qlow[NQ];
+    float lsum[4][R];
+    Seg seg[NQ + 1];   // the producer's own
+    Item<NQ> item[2];
     int dead;
     uint32_t tmem;
     uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], s_free[2], p_full, pv_done, wind_down[2];
+    uint64_t item_full[2], item_empty[2], q_full[2];
 };
 
 // The issuing warp runs its loop converged and one elected lane (lead != 0) issues: descriptors then stay in
@@ -211,6 +222,7 @@ __device__ __forceinline__ int stored_end(const csa2_pages& pg, int b) {
 
 struct KernelArgs {
     PagesAttnParams p;
+    int items;        // blocks x splits; CTA i takes items i, i + gridDim.x, ...
     int unit_log2;    // keys of a TMA box: 8 .. 128, divides every page
     int splits;
     int test_starve;  // test hook (csa2_test_starve_copies): the producer issues no copies
@@ -221,7 +233,7 @@ struct KernelArgs {
 // NQ queries, ST tiles in flight, the order of a tile's atoms, whether the three terms of P have accumulator columns
 // of their own (one product for all three, 3R columns, where TMEM has room), CTAs on an SM.
 template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas>
-__global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
+__global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     pages_attn_kernel(const __grid_constant__ CUtensorMap map_own, const __grid_constant__ CUtensorMap map_prefix,
                       const __grid_constant__ KernelArgs args) {
     using Sm = Smem<NQ, ST>;
@@ -234,7 +246,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
     extern __shared__ uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const PagesAttnParams& p = args.p;
-    constexpr int kProducer = 4 * NQ, kIssuer = kProducer + 1;   // warps behind the softmax warpgroups
+    constexpr int kProducer = 0, kIssuer = 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ul = args.unit_log2, unit = 1 << ul, upt = kTileKeys >> ul;   // keys of a unit, units of a tile
 
@@ -245,32 +257,28 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                 mbar_init(&sm.full[s][c], c == 0 ? 2 : 1);   // with the first part come the scales
                 mbar_init(&sm.empty[s][c], 1);
             }
-        mbar_init(&sm.s_full[0], 1);
-        mbar_init(&sm.s_full[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4 * NQ);
+            mbar_init(&sm.wind_down[i], 1);
+            mbar_init(&sm.item_full[i], 1);
+            mbar_init(&sm.item_empty[i], 4 * NQ + 2);
+            mbar_init(&sm.q_full[i], 4 * NQ);
+        }
         mbar_init(&sm.p_full, kWg * NQ);
         mbar_init(&sm.pv_done, 1);
-        mbar_init(&sm.wind_down[0], 1);
-        mbar_init(&sm.wind_down[1], 1);
-        mbar_init(&sm.s_free[0], 4 * NQ);
-        mbar_init(&sm.s_free[1], 4 * NQ);
         fence_mbar_init();
         sm.dead = 0;
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
     pdl_enter();
 
-    // ---- this CTA's queries ----
-    const bool shared_prefix = p.prefix.B != 0;
-    int f0, nq;   // first query (b Q + q) and count
-    if (shared_prefix) {
-        f0 = blockIdx.y * NQ;
-        nq = min(NQ, p.B * p.Q - f0);
-    } else {
-        const int per = (p.Q + NQ - 1) / NQ, b = blockIdx.y / per, q0 = (blockIdx.y % per) * NQ;
-        f0 = b * p.Q + q0;
-        nq = min(NQ, p.Q - q0);
-    }
-
-    // A bounded wait; the first to run out of time tells every other.
+    // A bounded wait; the first to run out of time tells every other.  From then on softmax threads pass their waits and
+    // arrive for work that was not done, so the producer and the issuers, who act on those arrivals, look at `dead`
+    // after every wait: a stage that never filled must not be armed again (its barrier's count would run below zero).
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t start = globaltimer_ns();
@@ -286,14 +294,23 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             }
         }
     };
+    auto is_dead = [&] { return *(volatile int*)&sm.dead != 0; };
+    const bool shared_prefix = p.prefix.B != 0;
+    auto queries_of = [&](int block, int& f0, int& nq) {
+        if (shared_prefix) {
+            f0 = block * NQ;
+            nq = min(NQ, p.B * p.Q - f0);
+        } else {
+            const int per = (p.Q + NQ - 1) / NQ, b = block / per, q0 = (block - b * per) * NQ;
+            f0 = b * p.Q + q0;
+            nq = min(NQ, p.Q - q0);
+        }
+    };
+    int nseg = 0;
     auto seg_of = [&](int tile) -> int {
         int s = 0;
-        while (s + 1 < sm.nseg && tile >= sm.seg[s + 1].tile0) ++s;
+        while (s + 1 < nseg && tile >= sm.seg[s + 1].tile0) ++s;
         return s;
-    };
-    auto first_tile = [&](int ntiles, int split) {   // the first ntiles % splits CTAs take one tile more
-        const int q = ntiles / args.splits, r = ntiles - q * args.splits;
-        return split * q + min(split, r);
     };
     // Producer: the copies of tile t, the CTA's n-th, part by part (one lane per unit), and the keys' scales.
     auto load_tile = [&](int t, int n) -> bool {
@@ -323,7 +340,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) {
             bool ok = true;
-            if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
+            if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1)) && !is_dead();
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
             if (c == 0) {
                 if (lane < upt) sm.upos[st][lane] = row >= 0 ? first : 0x7FFFFF00;
@@ -347,7 +364,17 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
     };
 
     if (warp == kProducer) {
-        // lanes 0 .. NQ-1: a query each; then lane 0 writes the lists
+        // ---- producer: an item's key lists and its tiles' copies.  It runs ahead of the others, so that an item's
+        // chain of loads (positions, page table, rows) passes under the item before.
+        int tile_no = 0;
+        bool ok = true;
+        for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
+        if (k >= 2) ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_empty[k & 1], (uint32_t)((k / 2 - 1) & 1)));
+        if (!ok) break;
+        const int block = it / args.splits, split = it - block * args.splits;
+        int f0, nq;
+        queries_of(block, f0, nq);
+        // lanes 0 .. NQ-1: a query each
         int i = -1, low = 0, end = 0, pend = 0;
         const int b = (f0 + min(lane, nq - 1)) / p.Q;
         if (lane < nq) i = p.q_pos[f0 + lane];
@@ -357,9 +384,10 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
         int64_t lw = p.window == 0x7FFFFFFF ? 0 : (int64_t)i - p.window + 1;
         if (p.replay_start && lane < nq) lw = max(lw, (int64_t)p.replay_start[b]);
         low = (int)max(lw, (int64_t)0);
+        Item<NQ>& item = sm.item[k & 1];
         if (lane < NQ) {
-            sm.qi[lane] = i;
-            sm.qlow[lane] = low;
+            item.qi[lane] = i;
+            item.qlow[lane] = low;
         }
         // Each lane's run of queries of one sequence: its extent and what its keys range over (every lane < nq alike).
         const bool mine = lane < nq;
@@ -416,79 +444,29 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             }
             if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow);
         }
+        nseg = n;
+        const int each = tiles / args.splits, extra = tiles - each * args.splits;   // the first splits take one tile more
+        const int t0 = split * each + min(split, extra), nt = each + (split < extra);
         if (lane == 0) {
-            sm.nseg = n;
-            sm.ntiles = tiles;
+            item.f0 = f0;
+            item.nq = nq;
+            item.tiles = nt;
+            item.part = it;
         }
-    } else if (warp < kProducer) {
-        // Q: a warp per row; 16 channels per lane -> E4M3 hi and lo, scaled so that the row's largest is in [2^7, 2^8).
-        // All of a warp's rows are loaded before the first is converted.
-        uint4 v[4][2];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = warp + 4 * NQ * k, c = r >> 4;
-            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-            if (c < nq) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(f0 + c) * kH + (r & 15)) * kD) + 2 * lane;
-                v[k][0] = __ldg(src);
-                v[k][1] = __ldg(src + 1);
-            }
-        }
-        float top[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = redux_max(top[k]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = warp + 4 * NQ * k, c = r >> 4, h = r & 15;
-            const int e = max((int)((__float_as_uint(top[k]) >> 23) & 0xFFu) - 127 - 7, -120);
-            const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4& vv = v[k][j >> 1];
-                const uint32_t w0 = (j & 1) ? vv.z : vv.x, w1 = (j & 1) ? vv.w : vv.y;
-                const float x[4] = {__uint_as_float(w0 << 16) * mul, __uint_as_float(w0 & 0xFFFF0000u) * mul,
-                                    __uint_as_float(w1 << 16) * mul, __uint_as_float(w1 & 0xFFFF0000u) * mul};
-                uint16_t a, b2;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1]), "f"(x[0]));
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3]), "f"(x[2]));
-                hi[j] = (uint32_t)a | ((uint32_t)b2 << 16);
-                float y[4];
-                e4m3x4_to_f32(hi[j], y);
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1] - y[1]), "f"(x[0] - y[0]));
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3] - y[3]), "f"(x[2] - y[2]));
-                lo[j] = (uint32_t)a | ((uint32_t)b2 << 16);
-            }
-            const int rh = 32 * c + h, rl = rh + 16, chunk = lane & 7;
-            *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (lane == 0) {
-                sm.rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
-                sm.mref[r] = -INFINITY;
-            }
-        }
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    if (warp == kProducer) {   // needs nothing of the others: its copies go out while Q is converted
         __syncwarp();
-        asm volatile("bar.arrive 15, %0;" ::"n"(kWg * NQ + 96) : "memory");
-    } else {
-        asm volatile("bar.sync 15, %0;" ::"n"(kWg * NQ + 96) : "memory");
-    }
-    tc_fence_after();
-    const uint32_t tmem = warp == kProducer ? 0u : sm.tmem;
-    const int ntiles = sm.ntiles;
-    const int t0 = first_tile(ntiles, blockIdx.x), t1 = first_tile(ntiles, blockIdx.x + 1), nt = t1 - t0;
-
-    if (warp == kProducer) {
-        int n = 0;
-        while (n < nt && load_tile(t0 + n, n)) ++n;
-        if (*(volatile int*)&sm.dead) {   // wind down: the copies in flight land before the CTA ends
-            for (int k = max(0, n - ST + 1); k <= min(n, nt - 1); ++k)
-                for (int c = 0; c < kBlocks; ++c) mbar_wait(&sm.full[k % ST][c], (uint32_t)((k / ST) & 1), kTimeoutNs / 8);
+        if (lane == 0) {
+            mbar_arrive(&sm.item_full[k & 1]);
+            if (it + gridDim.x < args.items) {   // the next item's queries on their way to L2
+                int g0, gn;
+                queries_of((it + gridDim.x) / args.splits, g0, gn);
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + (int64_t)g0 * kH * kD), "r"(gn * kH * kD * 2) : "memory");
+            }
+        }
+        for (int t = 0; ok && t < nt; ++t, ++tile_no) ok = load_tile(t0 + t, tile_no);
+        }
+        if (!ok) {   // wind down: the copies in flight land before the CTA ends
+            for (int n = max(0, tile_no - ST); n <= tile_no; ++n)
+                for (int c = 0; c < kBlocks; ++c) mbar_wait(&sm.full[n % ST][c], (uint32_t)((n / ST) & 1), kTimeoutNs / 16);
         }
     } else if (warp == kIssuer) {
         // ---- S issuer.  S and O have a warp each: one thread issues a product in about 50 cycles, more than most of
@@ -498,32 +476,37 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
         const uint32_t k0 = smem_u32(sm.K[0]);
         const uint64_t qd = smem_desc(smem_u32(sm.Qs), 16, 1024, kSw128);
         bool ok = true;
-        for (int n = 0; n < nt && ok; ++n) {
+        int n = 0;
+        for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
+        ok = wait(&sm.item_full[k & 1], (uint32_t)((k >> 1) & 1)) && wait(&sm.q_full[k & 1], (uint32_t)((k >> 1) & 1));
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
+        for (; n < last && ok; ++n) {
             const int st = n % ST;
             if (n >= 2) ok = wait(&sm.s_free[n & 1], (uint32_t)((n / 2 - 1) & 1));
-            ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1)) && ok;
-            __syncwarp();
+            const int first_parts = kByKeys ? kBlocks : 1;
+#pragma unroll
+            for (int c = 0; c < first_parts; ++c) ok = ok && wait(&sm.full[st][c], (uint32_t)((n / ST) & 1));
+            ok = __all_sync(0xFFFFFFFFu, ok && !is_dead());
+            if (!ok) break;
             const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
             const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
             const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
-            if (kByKeys) {
-#pragma unroll
-                for (int c = 1; c < kBlocks; ++c) ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
-                __syncwarp();
-            }
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c) {
                 if (!kByKeys && c > 0) {
-                    ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
-                    __syncwarp();
+                    ok = __all_sync(0xFFFFFFFFu, wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && !is_dead());
+                    if (!ok) break;
                 }
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                     mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
             }
+            if (!ok) break;
             commit(lead, &sm.s_full[n & 1]);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+        if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
         }
         if (!ok) {   // wind down: no product in flight when TMEM is freed
             commit(lead, &sm.wind_down[0]);
@@ -537,10 +520,14 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
         const uint32_t k0 = smem_u32(sm.K[0]);
         const uint64_t pd = smem_desc(smem_u32(sm.P), 128, 2048, kLayoutNone);
         bool ok = true;
-        for (int n = 0; n < nt && ok; ++n) {
+        int n = 0;
+        for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
+        ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_full[k & 1], (uint32_t)((k >> 1) & 1)));
+        const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
+        for (; n < last && ok; ++n) {
             const int st = n % ST;
-            ok = wait(&sm.p_full, (uint32_t)(n & 1));
-            __syncwarp();
+            ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full, (uint32_t)(n & 1)) && !is_dead());
+            if (!ok) break;
             const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
             const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
             const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128);
@@ -569,37 +556,101 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                 });
             }
             commit(lead, &sm.pv_done);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+        if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
         }
         if (!ok) {
             commit(lead, &sm.wind_down[1]);
             mbar_wait(&sm.wind_down[1], 0);
         }
         __syncwarp();
-    } else {
+    } else if (warp >= kAux / 32) {
         // ---- softmax: warpgroup = query, thread = key ----
-        const int wg = warp >> 2, key = tid & (kWg - 1), quarter = warp & 3;
+        const int wg = (warp - kAux / 32) >> 2, key = tid & (kWg - 1), quarter = warp & 3;
         const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
-        const int qi = sm.qi[wg], qlow = sm.qlow[wg];
         // this query's accumulator columns: 16 of each channel block (and of each term)
         auto ocol = [&](int b, int x) -> uint32_t { return tq + b * kOCols + x * R + kH * wg; };
         constexpr int kTerms = kConcat ? 3 : 1;
+        auto row4 = [&](const float (&a)[R], int j) { return *reinterpret_cast<const float4*>(&a[kH * wg + 4 * j]); };
+        const int ku = key >> ul, ko = key & (unit - 1);
+        int n = 0;
+        for (int k_item = 0, it = blockIdx.x; it < args.items; ++k_item, it += gridDim.x) {
+        const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
+        if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
+        const Item<NQ>& item = sm.item[k_item & 1];
+        const int f0 = item.f0, nq = item.nq, nt = item.tiles, qi = item.qi[wg], qlow = item.qlow[wg];
+        const int64_t part = item.part;
         {
             uint32_t zero[16] = {};
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                 for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
-            tmem_st_wait();
         }
+        {
+        // Q: a row (head) of this query at a time, 16 channels per lane -> E4M3 hi and lo, scaled so that the row's
+        // largest is in [2^7, 2^8).  All four rows are loaded before the first is converted.  The item before is done
+        // with the memory: each of its tiles' S has been seen.
+        uint4 v[4][2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+            if (wg < nq) {
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(f0 + wg) * kH + quarter + 4 * k) * kD) + 2 * lane;
+                v[k][0] = __ldg(src);
+                v[k][1] = __ldg(src + 1);
+            }
+        }
+        float top[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top[k] = redux_max(top[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int h = quarter + 4 * k, r = kH * wg + h;
+            const int e = max((int)((__float_as_uint(top[k]) >> 23) & 0xFFu) - 127 - 7, -120);
+            const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4& vv = v[k][j >> 1];
+                const uint32_t w0 = (j & 1) ? vv.z : vv.x, w1 = (j & 1) ? vv.w : vv.y;
+                const float x[4] = {__uint_as_float(w0 << 16) * mul, __uint_as_float(w0 & 0xFFFF0000u) * mul,
+                                    __uint_as_float(w1 << 16) * mul, __uint_as_float(w1 & 0xFFFF0000u) * mul};
+                uint16_t a, b2;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1]), "f"(x[0]));
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3]), "f"(x[2]));
+                hi[j] = (uint32_t)a | ((uint32_t)b2 << 16);
+                float y[4];
+                e4m3x4_to_f32(hi[j], y);
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1] - y[1]), "f"(x[0] - y[0]));
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3] - y[3]), "f"(x[2] - y[2]));
+                lo[j] = (uint32_t)a | ((uint32_t)b2 << 16);
+            }
+            const int rh = 32 * wg + h, rl = rh + 16, chunk = lane & 7;
+            *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (lane == 0) {
+                sm.rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
+                sm.mref[r] = -INFINITY;
+            }
+        }
+        }
+        fence_proxy_async_smem();
+        tmem_st_wait();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&sm.q_full[k_item & 1]);
+            mbar_arrive(&sm.item_empty[k_item & 1]);
+        }
+        wg_bar(wg);   // rowf and mref of the whole query
         float l[kH];
 #pragma unroll
         for (int h = 0; h < kH; ++h) l[h] = 0.0f;
-        auto row4 = [&](const float (&a)[R], int j) { return *reinterpret_cast<const float4*>(&a[kH * wg + 4 * j]); };
-        const int ku = key >> ul, ko = key & (unit - 1);
 
         // After a wait that ran out the loop goes on with what is there: every thread passes every barrier.
-        for (int n = 0; n < nt; ++n) {
+        for (int i = 0; i < nt; ++i, ++n) {
             const int st = n % ST;
             wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
             const Tile tile = sm.tile[st];
@@ -641,8 +692,8 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                         for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
                     }
                 };
-                bool move = n == 0;
-                if (n > 0) {
+                bool move = i == 0;
+                if (i > 0) {
                     relative();
                     float top = x[0];
 #pragma unroll
@@ -674,7 +725,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                         sm.mref[r] = fmaxf(m, old);
                     }
                     wg_bar(wg);
-                    if (n > 0) {
+                    if (i > 0) {
                         wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
                         tc_fence_after();
 #pragma unroll
@@ -690,8 +741,10 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                             }
                         tmem_st_wait();
                     }
+                    if (i > 0) {
 #pragma unroll
-                    for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
+                        for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
+                    }
                     relative();
                 }
                 const float tp = ts * kPScale;
@@ -720,7 +773,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                 wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
             }
             if (!active && lane == 0) mbar_arrive(&sm.s_free[n & 1]);
-            if (dirty) {   // S of this tile is done: only P K still reads the row
+            if (dirty && !is_dead()) {   // S of this tile is done: only P K still reads the row
                 for (int b = wg - tile.qa; b < kBlocks; b += tile.nq)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -747,15 +800,14 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
                 }
             }
             v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);   // lane i: row i & 15
-            wg_bar(wg);   // wmax of the last tile has been read
-            if (lane < kH) sm.wmax[quarter][kH * wg + lane] = v[0];
+            if (lane < kH) sm.lsum[quarter][kH * wg + lane] = v[0];
         }
         wg_bar(wg);
         if (key < kH) {
             const int r = kH * wg + key;
-            const float sum = (sm.wmax[0][r] + sm.wmax[1][r]) + (sm.wmax[2][r] + sm.wmax[3][r]), ref = sm.mref[r];
+            const float sum = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]), ref = sm.mref[r];
             if (args.splits > 1) {
-                float* ml = args.part_ml + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + r) * 2;
+                float* ml = args.part_ml + (part * R + r) * 2;
                 *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
             } else if (p.lse && wg < nq) {
                 p.lse[(int64_t)(f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
@@ -763,7 +815,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
         }
         wg_bar(wg);
-        if (nt > 0) wait(&sm.pv_done, (uint32_t)((nt - 1) & 1));
+        if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
         tc_fence_after();
         float fac[kH];
 #pragma unroll
@@ -771,7 +823,7 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             const float4 f = row4(sm.fac, j);
             fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
         }
-        float* po = args.part_o + (((int64_t)blockIdx.y * args.splits + blockIdx.x) * R + kH * wg) * kD;
+        float* po = args.part_o + (part * R + kH * wg) * kD;
         // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
         uint16_t* out = p.out + ((int64_t)(f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
 #pragma unroll
@@ -801,6 +853,8 @@ __global__ void __launch_bounds__(kWg * NQ + 96, kCtas)
             }
         }
         tc_fence_before();
+        wg_bar(wg);   // fac and mref are free for the next item
+        }
     }
     __syncthreads();
     if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
@@ -940,13 +994,13 @@ cudaError_t pool_map(const csa2_pages& pg, int unit, bool by_keys, CUtensorMap* 
 }
 
 template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas>
-cudaError_t launch(const KernelArgs& a, int blocks, const CUtensorMap& own, const CUtensorMap& prefix, cudaStream_t st) {
+cudaError_t launch(const KernelArgs& a, const CUtensorMap& own, const CUtensorMap& prefix, cudaStream_t st) {
     static DeviceOnce attr;
     const auto kernel = pages_attn_kernel<NQ, ST, kByKeys, kConcat, kCtas>;
-    const int smem = (int)sizeof(Smem<NQ, ST>) + 1024;
+    const int smem = (int)sizeof(Smem<NQ, ST>) + 1024, most = device_sm_count() * kCtas;
     cudaError_t e = attr.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
-    return launch_ex(kernel, dim3(a.splits, blocks), dim3(kWg * NQ + 96), smem, st, 0, own, prefix, a);
+    return launch_ex(kernel, dim3(most > 0 && a.items > most ? most : a.items), dim3(kWg * NQ + kAux), smem, st, 0, own, prefix, a);
 }
 
 }  // namespace
@@ -959,6 +1013,7 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
     KernelArgs a{};
     a.p = p;
     a.splits = pl.splits;
+    a.items = pl.blocks * pl.splits;
     a.test_starve = test_starve_copies();
     a.part_o = (float*)ws;
     a.part_ml = (float*)((char*)ws + pl.o_bytes);
@@ -978,10 +1033,10 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
         e = pool_map(p.prefix, unit, by_keys, &mp);
         if (e != cudaSuccess) return e;
     }
-    e = pl.nq == 1   ? launch<1, 1, true, true, 2>(a, pl.blocks, mo, mp, st)
-        : pl.nq == 2 ? launch<2, 1, true, false, 2>(a, pl.blocks, mo, mp, st)
-        : by_keys    ? launch<4, 2, true, false, 1>(a, pl.blocks, mo, mp, st)
-                     : launch<4, 2, false, false, 1>(a, pl.blocks, mo, mp, st);
+    e = pl.nq == 1   ? launch<1, 1, true, true, 2>(a, mo, mp, st)
+        : pl.nq == 2 ? launch<2, 1, true, false, 2>(a, mo, mp, st)
+        : by_keys    ? launch<4, 2, true, false, 1>(a, mo, mp, st)
+                     : launch<4, 2, false, false, 1>(a, mo, mp, st);
     if (e != cudaSuccess || pl.splits == 1) return e;
     return launch_ex(pages_merge_kernel, dim3((unsigned)(p.B * p.Q * kH)), dim3(128), 0, st, 0, a, pl.nq);
 }

@@ -452,3 +452,26 @@ def test_refusals_on_the_device(csa):
     with pytest.raises(csa.CSA2Error):
         csa.csa2_pages_append(torch.zeros(4, 516, dtype=torch.bfloat16).cuda()[:, :D], pages,
                               torch.zeros(4, dtype=torch.int32).cuda(), torch.zeros(4, dtype=torch.int32).cuda())
+
+
+def test_timeout_is_reported(csa):
+    """A producer that issues no copies (the library's test hook): the waits run out after 2 s, the call ends, the flag is
+    set and read, and the next call on the same context is right again."""
+    cache = Cache(90, [300, 90], 64)
+    q, q_pos = queries(3, 2, 1), tail_positions([300, 90], 1)
+    prefix = Cache(91, [700], 64)
+    own = Cache(92, [5, 9], 64, pos0=700)
+    pq_pos = np.array([[704], [708]], np.int32)
+    csa.csa2_flag_status()
+    for call in (lambda: csa.csa2_window_attn(q.cuda(), cache.gpu(), torch.from_numpy(q_pos).cuda()),
+                 lambda: csa.csa2_prefix_attn(q.cuda(), prefix.gpu(), own.gpu(), torch.from_numpy(pq_pos).cuda())):
+        csa.lib().csa2_test_starve_copies(1)
+        try:
+            call()
+            with pytest.raises(csa.CSA2Error, match="TIMEOUT"):
+                csa.csa2_flag_status(clear=True)
+        finally:
+            csa.lib().csa2_test_starve_copies(0)
+        csa.csa2_flag_status()
+    check(*run_window(csa, cache, q, q_pos, 128, 4), reference(q, q_pos, [(cache, True)], 128, 4))
+    check(*run_prefix(csa, prefix, own, q, pq_pos), reference(q, pq_pos, [(prefix, False), (own, True)]))
