@@ -35,7 +35,7 @@ constexpr int kTileKeys = 128;
 constexpr int kGroup = 8;                              // keys of one swizzle atom
 constexpr int kBlocks = kD / 128;                      // channel blocks of 128 channels: 128 bytes, a swizzle row
 constexpr int kTileBytes = kTileKeys * kD;             // 64 KB
-constexpr int kAux = 128;                              // producer, S issuer, O issuer and an idle warp: the oldest, which issue first
+constexpr int kAux = 96;                               // producer, S issuer, O issuer
 constexpr int kWg = 128;                               // threads of a softmax warpgroup: one query, a thread per key
 constexpr float kHeadroom = 3.0f;                      // log2 of how far a weight may exceed the reference
 constexpr float kPScale = 4096.0f;                     // weight 1 at 2^12, 2^15 with the headroom: below f16's and E5M2's largest
@@ -92,7 +92,6 @@ struct Layout {
 // A CTA's item (queries and a split of their keys): what the producer tells the other roles.
 template <int NQ>
 struct Item {
-    int f0, nq;     // first query (b Q + q) and count
     int tiles;
     int64_t part;   // block * splits + split
     int qi[NQ], qlow[NQ];   // each query's token, and the first that its window holds
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     extern __shared__ uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const PagesAttnParams& p = args.p;
-    constexpr int kProducer = 0, kIssuer = 1;
+    constexpr int kProducer = 4 * NQ, kIssuer = kProducer + 1;   // behind the softmax warpgroups
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ul = args.unit_log2, unit = 1 << ul, upt = kTileKeys >> ul;   // keys of a unit, units of a tile
 
@@ -448,8 +447,6 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         const int each = tiles / args.splits, extra = tiles - each * args.splits;   // the first splits take one tile more
         const int t0 = split * each + min(split, extra), nt = each + (split < extra);
         if (lane == 0) {
-            item.f0 = f0;
-            item.nq = nq;
             item.tiles = nt;
             item.part = it;
         }
@@ -564,9 +561,9 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             mbar_wait(&sm.wind_down[1], 0);
         }
         __syncwarp();
-    } else if (warp >= kAux / 32) {
+    } else {
         // ---- softmax: warpgroup = query, thread = key ----
-        const int wg = (warp - kAux / 32) >> 2, key = tid & (kWg - 1), quarter = warp & 3;
+        const int wg = warp >> 2, key = tid & (kWg - 1), quarter = warp & 3;
         const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
         // this query's accumulator columns: 16 of each channel block (and of each term)
         auto ocol = [&](int b, int x) -> uint32_t { return tq + b * kOCols + x * R + kH * wg; };
@@ -575,22 +572,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         const int ku = key >> ul, ko = key & (unit - 1);
         int n = 0;
         for (int k_item = 0, it = blockIdx.x; it < args.items; ++k_item, it += gridDim.x) {
-        const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
-        if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
-        const Item<NQ>& item = sm.item[k_item & 1];
-        const int f0 = item.f0, nq = item.nq, nt = item.tiles, qi = item.qi[wg], qlow = item.qlow[wg];
-        const int64_t part = item.part;
-        {
-            uint32_t zero[16] = {};
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
-        }
-        {
-        // Q: a row (head) of this query at a time, 16 channels per lane -> E4M3 hi and lo, scaled so that the row's
-        // largest is in [2^7, 2^8).  All four rows are loaded before the first is converted.  The item before is done
-        // with the memory: each of its tiles' S has been seen.
+        int f0, nq;
+        queries_of(it / args.splits, f0, nq);
         uint4 v[4][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -601,6 +584,21 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 v[k][1] = __ldg(src + 1);
             }
         }
+        const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
+        if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
+        const Item<NQ>& item = sm.item[k_item & 1];
+        const int nt = item.tiles, qi = item.qi[wg], qlow = item.qlow[wg];
+        const int64_t part = item.part;
+        {
+            uint32_t zero[16] = {};
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
+        }
+        {
+        // Q: a row (head) of this query at a time, 16 channels per lane -> E4M3 hi and lo, scaled so that the row's
+        // largest is in [2^7, 2^8).  The item before is done with the memory: each of its tiles' S has been seen.
         float top[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
