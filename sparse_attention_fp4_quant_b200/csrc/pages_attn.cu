@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     if (tid == 32 * kProducer) {
         for (int s = 0; s < ST; ++s)
             for (int c = 0; c < kBlocks; ++c) {
-                mbar_init(&sm.full[s][c], c == 0 ? 2 : 1);   // with the first part come the scales
+                mbar_init(&sm.full[s][c], kByKeys && c == 0 ? 2 : 1);   // with the first part come the scales
                 mbar_init(&sm.empty[s][c], 1);
             }
         for (int i = 0; i < 2; ++i) {
@@ -275,9 +275,9 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     const uint32_t tmem = sm.tmem;
     pdl_enter();
 
-    // A bounded wait; the first to run out of time tells every other.  From then on softmax threads pass their waits and
-    // arrive for work that was not done, so the producer and the issuers, who act on those arrivals, look at `dead`
-    // after every wait: a stage that never filled must not be armed again (its barrier's count would run below zero).
+    // A bounded wait; the first to run out of time tells every other.  From then on producer and issuers stop, and softmax
+    // threads pass their waits but arrive for nothing any more: a stage that never filled must not be freed and armed
+    // again (its barrier's count would run below zero).
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t start = globaltimer_ns();
@@ -293,7 +293,6 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             }
         }
     };
-    auto is_dead = [&] { return *(volatile int*)&sm.dead != 0; };
     const bool shared_prefix = p.prefix.B != 0;
     auto queries_of = [&](int block, int& f0, int& nq) {
         if (shared_prefix) {
@@ -311,7 +310,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         while (s + 1 < nseg && tile >= sm.seg[s + 1].tile0) ++s;
         return s;
     };
-    // Producer: the copies of tile t, the CTA's n-th, part by part (one lane per unit), and the keys' scales.
+    // Producer: the copies of tile t, the CTA's n-th, part by part (one lane per unit), and the keys' scales: by a copy
+    // per unit where units are large, else by the lanes' own loads (a copy costs about 50 cycles however small).
     auto load_tile = [&](int t, int n) -> bool {
         const int st = n % ST;
         const Seg& sg = sm.seg[seg_of(t)];
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         }
         const int row4 = __shfl_sync(0xFFFFFFFFu, row, (4 * lane) >> ul);   // the unit of keys 4 lane .. 4 lane + 3
         float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (row4 >= 0) sc = __ldg(reinterpret_cast<const float4*>(sg.scales + row4 + ((4 * lane) & (unit - 1))));
+        if (kByKeys && row4 >= 0) sc = __ldg(reinterpret_cast<const float4*>(sg.scales + row4 + ((4 * lane) & (unit - 1))));
         const uint32_t live = __ballot_sync(0xFFFFFFFFu, row >= 0);
         const int first = sg.pos0 + sg.unit(v) * unit, last = first + unit - 1;
         const bool inside = row >= 0 && last < sg.end && last <= sg.imin && (first >= sg.lmax || (sg.own && last < p.n_sink));
@@ -339,26 +339,27 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) {
             bool ok = true;
-            if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1)) && !is_dead();
+            if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
             if (c == 0) {
                 if (lane < upt) sm.upos[st][lane] = row >= 0 ? first : 0x7FFFFF00;
                 if (lane == 0) sm.tile[st] = info;
             }
             const int upp = 32 >> ul;   // by keys: units of a part
-            const uint32_t bytes = kByKeys ? __popc(live & (((1u << upp) - 1u) << (c * upp))) * unit * kD : __popc(live) * unit * 128;
+            const uint32_t bytes = kByKeys ? __popc(live & (((1u << upp) - 1u) << (c * upp))) * unit * kD : __popc(live) * unit * (c == 0 ? 128 + 4 : 128);
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], bytes);
             __syncwarp();
             if (row >= 0 && !args.test_starve) {
-                if (!kByKeys)
+                if (!kByKeys) {
                     tma_unit(sm.K[st] + c * L::block + lane * unit * 128, map, row, c, &sm.full[st][c]);
-                else if (lane >> (5 - ul) == c)
+                    if (c == 0) bulk_load(&sm.sc[st][lane * unit], sg.scales + row, unit * 4, &sm.full[st][0]);
+                } else if (lane >> (5 - ul) == c)
                     tma_groups(sm.K[st] + lane * unit * kD, map, row / kGroup, &sm.full[st][c]);
             }
-            if (c == 0 && n >= ST) put_scales();
+            if (kByKeys && c == 0 && n >= ST) put_scales();
         }
-        if (n < ST) put_scales();   // the first tiles: the copies go out before the scales are back
+        if (kByKeys && n < ST) put_scales();   // the first tiles: the copies go out before the scales are back
         return true;
     };
 
@@ -484,22 +485,23 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             const int first_parts = kByKeys ? kBlocks : 1;
 #pragma unroll
             for (int c = 0; c < first_parts; ++c) ok = ok && wait(&sm.full[st][c], (uint32_t)((n / ST) & 1));
-            ok = __all_sync(0xFFFFFFFFu, ok && !is_dead());
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
             const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
             const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c) {
-                if (!kByKeys && c > 0) {
-                    ok = __all_sync(0xFFFFFFFFu, wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && !is_dead());
-                    if (!ok) break;
+                if (!kByKeys && c > 0) {   // after a wait that ran out the products read what is there; S is not announced
+                    ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
+                    __syncwarp();
                 }
                 tc_fence_after();
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                     mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
             }
+            if (!kByKeys) ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             commit(lead, &sm.s_full[n & 1]);
         }
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
         for (; n < last && ok; ++n) {
             const int st = n % ST;
-            ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full, (uint32_t)(n & 1)) && !is_dead());
+            ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full, (uint32_t)(n & 1)));
             if (!ok) break;
             const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
             const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
@@ -647,10 +649,10 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
 #pragma unroll
         for (int h = 0; h < kH; ++h) l[h] = 0.0f;
 
-        // After a wait that ran out the loop goes on with what is there: every thread passes every barrier.
+        // After a wait that ran out the loop goes on with what is there: every thread passes every named barrier.
         for (int i = 0; i < nt; ++i, ++n) {
             const int st = n % ST;
-            wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
+            bool ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
             const Tile tile = sm.tile[st];
             const bool active = wg >= tile.qa && wg < tile.qa + tile.nq;   // this tile's products cover this query
             bool seen = active;
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             }
             const float ts = seen ? sm.sc[st][key] : 0.0f;
             bool dirty = false;
-            wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1));
+            ok = wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1)) && ok;
             tc_fence_after();
             if (active) {
                 const float lsc = fmaxf(__log2f(ts), kMinLogScale);
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 dirty = !seen && z[0] != z[0];
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.s_free[n & 1]);
+                if (lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
                 auto relative = [&]() {   // the product rounded first, as in the maximum: huge logits still meet it exactly
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -762,16 +764,16 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     w[1][j] = __byte_perm(m0, m1, 0x7531);
                     w[2][j] = __byte_perm(l0, l1, 0x7531);
                 }
-                if (n > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));   // P is free when the last tile's products are done
+                if (n > 0) ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;   // P is free when the last tile's products are done
 #pragma unroll
                 for (int y = 0; y < 3; ++y)
                     *reinterpret_cast<uint4*>(&sm.P[y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
             } else if (n > 0) {
                 // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
-                wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+                ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;
             }
-            if (!active && lane == 0) mbar_arrive(&sm.s_free[n & 1]);
-            if (dirty && !is_dead()) {   // S of this tile is done: only P K still reads the row
+            if (!active && lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
+            if (dirty && ok) {   // S of this tile is done: only P K still reads the row
                 for (int b = wg - tile.qa; b < kBlocks; b += tile.nq)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             }
             fence_proxy_async_smem();
             tc_fence_before();
-            mbar_arrive(&sm.p_full);
+            if (ok) mbar_arrive(&sm.p_full);
         }
         // ---- row sums over the 128 threads, then the output ----
         {
