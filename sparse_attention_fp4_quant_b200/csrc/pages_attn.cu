@@ -209,7 +209,7 @@ __device__ __forceinline__ void split_e5m2(uint32_t p, uint32_t& hi, uint32_t& m
     const uint32_t rb = *reinterpret_cast<uint32_t*>(&r);
     mid = rb & 0xFF00FF00u;
     r = __hsub2(r, *reinterpret_cast<const __half2*>(&mid));
-    lo = (*reinterpret_cast<uint32_t*>(&r) + 0x00800080u) & 0xFF00FF00u;
+    lo = *reinterpret_cast<uint32_t*>(&r) + 0x00800080u;   // the low bytes are not used
 }
 
 __device__ __forceinline__ int stored_end(const csa2_pages& pg, int b) {
@@ -666,50 +666,51 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             tc_fence_after();
             if (active) {
                 const float lsc = fmaxf(__log2f(ts), kMinLogScale);
-                float z[kH], x[kH];   // z = q . k; x = z in log2 units less the row's reference
-                {
-                    uint32_t u[32];
+                float x[kH];   // logits in log2 units less the rows' references
+                auto sums = [&](uint32_t (&u)[32]) {   // hi in u[0 .. 15], lo in u[16 .. 31]
                     tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * R + 32 * wg, u);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int h = 0; h < kH; ++h) z[h] = (__uint_as_float(u[h]) + __uint_as_float(u[16 + h])) * ts;
-                }
-                dirty = !seen && z[0] != z[0];
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
-                auto relative = [&]() {   // the product rounded first, as in the maximum: huge logits still meet it exactly
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 f = row4(sm.rowf, j), m = row4(sm.mref, j);
-                        x[4 * j] = __fmul_rn(z[4 * j], f.x) - m.x;
-                        x[4 * j + 1] = __fmul_rn(z[4 * j + 1], f.y) - m.y;
-                        x[4 * j + 2] = __fmul_rn(z[4 * j + 2], f.z) - m.z;
-                        x[4 * j + 3] = __fmul_rn(z[4 * j + 3], f.w) - m.w;
-                    }
-                    if (!tile.interior) {
-#pragma unroll
-                        for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
-                    }
                 };
                 bool move = i == 0;
                 if (i > 0) {
-                    relative();
-                    float top = x[0];
+                    uint32_t u[32];
+                    sums(u);
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int h = 1; h < kH; ++h) top = fmaxf(top, x[h]);
-                    move = wg_any(wg, top + lsc > kHeadroom);
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 f4 = row4(sm.rowf, j), m4 = row4(sm.mref, j);
+                        const float f[4] = {f4.x, f4.y, f4.z, f4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int h = 4 * j + c;
+                            x[h] = fmaf(__uint_as_float(u[h]) + __uint_as_float(u[16 + h]), ts * f[c], -m[c]);
+                            top = fmaxf(top, x[h]);
+                        }
+                    }
+                    dirty = !seen && x[0] != x[0];
+                    move = wg_any(wg, seen && top + lsc > kHeadroom);
                 }
                 // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
                 if (__builtin_expect(move, 0)) {
+                    // here each product is rounded for itself, in the maximum as below: huge logits meet it exactly
                     float mx[kH];
+                    {
+                        uint32_t u[32];
+                        sums(u);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 f4 = row4(sm.rowf, j);
-                        const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 f4 = row4(sm.rowf, j);
+                            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mx[4 * j + i] = redux_max(seen ? __fmul_rn(z[4 * j + i], f[i]) + lsc : -INFINITY);
+                            for (int c = 0; c < 4; ++c) {
+                                const int h = 4 * j + c;
+                                x[h] = __fmul_rn(__fmul_rn(__uint_as_float(u[h]) + __uint_as_float(u[16 + h]), ts), f[c]);
+                            }
+                        }
                     }
+                    dirty = !seen && x[0] != x[0];
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) mx[h] = redux_max(seen ? x[h] + lsc : -INFINITY);
                     if (lane == 0) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -728,9 +729,9 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     if (i > 0) {
                         wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
+#pragma unroll 1
                             for (int y = 0; y < kTerms; ++y) {
                                 uint32_t o[16];
                                 tmem_ld_32x32b_x16(ocol(b, y), o);
@@ -745,8 +746,19 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
 #pragma unroll
                         for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
                     }
-                    relative();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 m = row4(sm.mref, j);
+                        x[4 * j] -= m.x, x[4 * j + 1] -= m.y, x[4 * j + 2] -= m.z, x[4 * j + 3] -= m.w;
+                    }
                 }
+                if (!tile.interior) {
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
                 const float tp = ts * kPScale;
                 uint32_t w[3][4];
 #pragma unroll
