@@ -109,7 +109,7 @@ struct Smem {
     alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
     alignas(16) float fac[R];
-    alignas(16) float rowf[R];
+    alignas(16) float rowf[2][R];   // by item
     float lsum[4][R];
     Seg seg[NQ + 1];   // the producer's own
     Item<NQ> item[2];
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         fence_mbar_init();
         sm.dead = 0;
     }
+    if (tid < R) sm.mref[tid] = -INFINITY;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -573,8 +574,18 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         auto row4 = [&](const float (&a)[R], int j) { return *reinterpret_cast<const float4*>(&a[kH * wg + 4 * j]); };
         const int ku = key >> ul, ko = key & (unit - 1);
         int n = 0;
-        for (int k_item = 0, it = blockIdx.x; it < args.items; ++k_item, it += gridDim.x) {
-        int f0, nq;
+        // Item by item: its queries are converted as soon as the item before has seen its last S, so that the first S
+        // of the next is made while the output of the last is written.
+        int f0 = 0, nq = 0, nt = 0, prev_f0 = 0, prev_nq = 0;
+        int64_t part = 0;
+        for (int k_item = 0, it = blockIdx.x;; ++k_item, it += gridDim.x) {
+        const bool have = it < args.items;
+        float(&rowf)[R] = sm.rowf[k_item & 1];
+        prev_f0 = f0;
+        prev_nq = nq;
+        if (have) {
+        // Q: four rows (heads) of this query in each warp, 16 channels per lane -> E4M3 hi and lo, each row scaled so that
+        // its largest is in [2^7, 2^8)
         queries_of(it / args.splits, f0, nq);
         uint4 v[4][2];
 #pragma unroll
@@ -588,19 +599,6 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         }
         const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
         if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
-        const Item<NQ>& item = sm.item[k_item & 1];
-        const int nt = item.tiles, qi = item.qi[wg], qlow = item.qlow[wg];
-        const int64_t part = item.part;
-        {
-            uint32_t zero[16] = {};
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
-        }
-        {
-        // Q: a row (head) of this query at a time, 16 channels per lane -> E4M3 hi and lo, scaled so that the row's
-        // largest is in [2^7, 2^8).  The item before is done with the memory: each of its tiles' S has been seen.
         float top[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
@@ -631,20 +629,86 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             const int rh = 32 * wg + h, rl = rh + 16, chunk = lane & 7;
             *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (lane == 0) {
-                sm.rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
-                sm.mref[r] = -INFINITY;
-            }
-        }
+            if (lane == 0)
+                rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
         }
         fence_proxy_async_smem();
-        tmem_st_wait();
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&sm.q_full[k_item & 1]);
-            mbar_arrive(&sm.item_empty[k_item & 1]);
+        if (lane == 0) mbar_arrive(&sm.q_full[k_item & 1]);
         }
-        wg_bar(wg);   // rowf and mref of the whole query
+        if (k_item > 0) {
+        // ---- the output of the item before ----
+        wg_bar(wg);
+        if (key < kH) {
+            const int r = kH * wg + key;
+            const float sum = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]), ref = sm.mref[r];
+            if (args.splits > 1) {
+                float* ml = args.part_ml + (part * R + r) * 2;
+                *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
+            } else if (p.lse && wg < prev_nq) {
+                p.lse[(int64_t)(prev_f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            }
+            sm.mref[r] = -INFINITY;   // for the next item
+            sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
+        }
+        wg_bar(wg);
+        if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+        tc_fence_after();
+        float fac[kH];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 f = row4(sm.fac, j);
+            fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
+        }
+        float* po = args.part_o + (part * R + kH * wg) * kD;
+        // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
+        uint16_t* out = p.out + ((int64_t)(prev_f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            uint32_t o[kTerms][16];
+#pragma unroll
+            for (int y = 0; y < kTerms; ++y) tmem_ld_32x32b_x16(ocol(b, y), o[y]);
+            tmem_ld_wait();
+            float y[kH];
+#pragma unroll
+            for (int h = 0; h < kH; ++h) {
+                y[h] = __uint_as_float(o[0][h]);
+#pragma unroll
+                for (int x = 1; x < kTerms; ++x) y[h] += __uint_as_float(o[x][h]);
+                y[h] *= fac[h];
+            }
+            if (args.splits > 1) {
+#pragma unroll
+                for (int h = 0; h < kH; ++h) po[h * kD + 128 * b + key] = y[h];
+            } else if (wg < prev_nq) {
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const uint32_t own = pack_bf16(y[h], y[h + 8]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                    *reinterpret_cast<uint32_t*>(out + h * kD + 128 * b) =
+                        (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                }
+            }
+        }
+        tc_fence_before();
+        wg_bar(wg);   // fac and mref are free
+        }
+        if (!have) break;
+
+        const Item<NQ>& item = sm.item[k_item & 1];
+        const int qi = item.qi[wg], qlow = item.qlow[wg];
+        nt = item.tiles;
+        part = item.part;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty[k_item & 1]);
+        {
+            uint32_t zero[16] = {};
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
+            tmem_st_wait();
+        }
+        wg_bar(wg);   // rowf of the whole query
         float l[kH];
 #pragma unroll
         for (int h = 0; h < kH; ++h) l[h] = 0.0f;
@@ -678,7 +742,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 f4 = row4(sm.rowf, j), m4 = row4(sm.mref, j);
+                        const float4 f4 = row4(rowf, j), m4 = row4(sm.mref, j);
                         const float f[4] = {f4.x, f4.y, f4.z, f4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -699,7 +763,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                         sums(u);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float4 f4 = row4(sm.rowf, j);
+                            const float4 f4 = row4(rowf, j);
                             const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
@@ -796,7 +860,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             tc_fence_before();
             if (ok) mbar_arrive(&sm.p_full);
         }
-        // ---- row sums over the 128 threads, then the output ----
+        // ---- row sums over the 128 threads ----
         {
             // halving exchange: after step o a lane holds the sums over lane pairs of half as many rows
             float v[kH];
@@ -814,58 +878,6 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);   // lane i: row i & 15
             if (lane < kH) sm.lsum[quarter][kH * wg + lane] = v[0];
         }
-        wg_bar(wg);
-        if (key < kH) {
-            const int r = kH * wg + key;
-            const float sum = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]), ref = sm.mref[r];
-            if (args.splits > 1) {
-                float* ml = args.part_ml + (part * R + r) * 2;
-                *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
-            } else if (p.lse && wg < nq) {
-                p.lse[(int64_t)(f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-            }
-            sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
-        }
-        wg_bar(wg);
-        if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
-        tc_fence_after();
-        float fac[kH];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 f = row4(sm.fac, j);
-            fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
-        }
-        float* po = args.part_o + (part * R + kH * wg) * kD;
-        // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
-        uint16_t* out = p.out + ((int64_t)(f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            uint32_t o[kTerms][16];
-#pragma unroll
-            for (int y = 0; y < kTerms; ++y) tmem_ld_32x32b_x16(ocol(b, y), o[y]);
-            tmem_ld_wait();
-            float y[kH];
-#pragma unroll
-            for (int h = 0; h < kH; ++h) {
-                y[h] = __uint_as_float(o[0][h]);
-#pragma unroll
-                for (int x = 1; x < kTerms; ++x) y[h] += __uint_as_float(o[x][h]);
-                y[h] *= fac[h];
-            }
-            if (args.splits > 1) {
-#pragma unroll
-                for (int h = 0; h < kH; ++h) po[h * kD + 128 * b + key] = y[h];
-            } else if (wg < nq) {
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const uint32_t own = pack_bf16(y[h], y[h + 8]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-                    *reinterpret_cast<uint32_t*>(out + h * kD + 128 * b) =
-                        (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-                }
-            }
-        }
-        tc_fence_before();
-        wg_bar(wg);   // fac and mref are free for the next item
         }
     }
     __syncthreads();
