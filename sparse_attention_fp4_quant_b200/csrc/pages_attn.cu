@@ -885,12 +885,19 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
 }
 
 // Joins the splits of a block: one CTA per row, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).  The weights
-// come first, a thread per split, so that the loads of the partial rows do not wait on one another.
-__global__ void __launch_bounds__(128) pages_merge_kernel(const __grid_constant__ KernelArgs args, int NQ) {
+// come first, a thread per split, so that the loads of the partial rows do not wait on one another.  With many splits
+// four groups of 128 threads take every fourth one (12 queries in 49 splits: 36 us in all against 44 with one group);
+// with few one group does (61 queries in 4 splits: 45.5 against 47.6).
+constexpr int kMergeMany = 12;   // splits from which on four groups join them
+template <int kGroups>
+__global__ void __launch_bounds__(128 * kGroups) pages_merge_kernel(const __grid_constant__ KernelArgs args, int NQ) {
     pdl_enter();
-    __shared__ float w[kMaxSplits], red[4], red2[4];
+    __shared__ float w[kMaxSplits], red[4 * kGroups], red2[4 * kGroups];
+    __shared__ float4 part[kGroups][128];
+    static_assert(kMaxSplits <= 512 && kMergeMany <= 128, "a thread per split");
     const PagesAttnParams& p = args.p;
     const int S = args.splits, R = kH * NQ, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = tid >> 7, col = tid & 127;
     const int f = blockIdx.x / kH, h = blockIdx.x % kH;
     int blk, c;
     if (p.prefix.B) {
@@ -902,46 +909,48 @@ __global__ void __launch_bounds__(128) pages_merge_kernel(const __grid_constant_
         c = q % NQ;
     }
     const int64_t r0 = ((int64_t)blk * S) * R + 16 * c + h;   // row of split s: r0 + s R
-    const float2* ml = reinterpret_cast<const float2*>(args.part_ml) + r0;
-    const float4* po = reinterpret_cast<const float4*>(args.part_o + r0 * kD) + tid;
-    float2 v[(kMaxSplits + 127) / 128];
-    float M = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < (kMaxSplits + 127) / 128; ++i) {
-        const int s = tid + 128 * i;
-        v[i] = s < S ? __ldcg(ml + (int64_t)s * R) : make_float2(-INFINITY, 0.0f);
-        M = fmaxf(M, v[i].x);
-    }
-    M = redux_max(M);
-    if (lane == 0) red[warp] = M;
+    const float2 v = tid < S ? __ldcg(reinterpret_cast<const float2*>(args.part_ml) + r0 + (int64_t)tid * R)
+                             : make_float2(-INFINITY, 0.0f);
+    const float wm = redux_max(v.x);
+    if (lane == 0) red[warp] = wm;
     __syncthreads();
-    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float Mu = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
+    float M = red[0];
 #pragma unroll
-    for (int i = 0; i < (kMaxSplits + 127) / 128; ++i) {
-        const int s = tid + 128 * i;
-        const float e = exp2f(v[i].x - Mu);
-        if (s < S) w[s] = e;
-        L = fmaf(v[i].y, e, L);
-    }
+    for (int i = 1; i < 4 * kGroups; ++i) M = fmaxf(M, red[i]);
+    const float Mu = M == -INFINITY ? 0.0f : M;
+    const float e = exp2f(v.x - Mu);
+    if (tid < S) w[tid] = e;
+    float L = v.y * e;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
     if (lane == 0) red2[warp] = L;
     __syncthreads();
-    L = (red2[0] + red2[1]) + (red2[2] + red2[3]);
+    const float4* po = reinterpret_cast<const float4*>(args.part_o + r0 * kD) + col;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-    for (int s = 0; s < S; ++s) {
+    for (int s = group; s < S; s += kGroups) {
         const float4 y = __ldcg(po + (int64_t)s * R * (kD / 4));
-        const float e = w[s];
-        o.x = fmaf(y.x, e, o.x);
-        o.y = fmaf(y.y, e, o.y);
-        o.z = fmaf(y.z, e, o.z);
-        o.w = fmaf(y.w, e, o.w);
+        const float ws = w[s];
+        o.x = fmaf(y.x, ws, o.x);
+        o.y = fmaf(y.y, ws, o.y);
+        o.z = fmaf(y.z, ws, o.z);
+        o.w = fmaf(y.w, ws, o.w);
+    }
+    L = red2[0];
+#pragma unroll
+    for (int i = 1; i < 4 * kGroups; ++i) L += red2[i];
+    if (kGroups > 1) {
+        if (group > 0) part[group][col] = o;
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) {
+            const float4 y = part[g][col];
+            o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+        }
     }
     const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    *reinterpret_cast<uint2*>(p.out + (int64_t)blockIdx.x * kD + 4 * tid) =
+    *reinterpret_cast<uint2*>(p.out + (int64_t)blockIdx.x * kD + 4 * col) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     if (p.lse && tid == 0) p.lse[blockIdx.x] = L > 0.0f ? (Mu + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
@@ -966,7 +975,8 @@ Plan plan(bool prefix, int B, int Q, int64_t keys) {
     pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
     const int64_t ctas = pl.two ? 2 * kSplitSMs : kSplitSMs;
     int64_t s = ctas / pl.blocks;
-    if (s > tiles / 2) s = tiles / 2;   // two tiles at least: a third costs a CTA less than the join does
+    const int64_t most = tiles < 4 ? 1 : tiles;   // up to three tiles cost a CTA less than the join does
+    if (s > most) s = most;
     if (s < 1) s = 1;
     pl.splits = (int)s;
     // One query: with few tiles and CTAs, all of them in flight at once (one token, 132 keys: 8.4 us against 9.6);
@@ -1066,7 +1076,9 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
         : by_keys    ? launch<4, 2, true, false, 1>(a, mo, mp, st)
                      : launch<4, 2, false, false, 1>(a, mo, mp, st);
     if (e != cudaSuccess || pl.splits == 1) return e;
-    return launch_ex(pages_merge_kernel, dim3((unsigned)(p.B * p.Q * kH)), dim3(128), 0, st, 0, a, pl.nq);
+    const dim3 rows((unsigned)(p.B * p.Q * kH));
+    return pl.splits < kMergeMany ? launch_ex(pages_merge_kernel<1>, rows, dim3(128), 0, st, 0, a, pl.nq)
+                                  : launch_ex(pages_merge_kernel<4>, rows, dim3(512), 0, st, 0, a, pl.nq);
 }
 
 }  // namespace csa2
