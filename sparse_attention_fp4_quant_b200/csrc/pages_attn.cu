@@ -38,7 +38,7 @@ constexpr int kTileBytes = kTileKeys * kD;             // 64 KB
 constexpr int kAux = 96;                               // producer, S issuer, O issuer
 constexpr int kWg = 128;                               // threads of a softmax warpgroup: one query, a thread per key
 constexpr float kHeadroom = 3.0f;                      // log2 of how far a weight may exceed the reference
-constexpr float kPScale = 4096.0f;                     // weight 1 at 2^12, 2^15 with the headroom: below f16's and E5M2's largest
+constexpr float kPScale = 4096.0f;                     // weight 1 at 2^12, 2^15 with the headroom: in range of f16, E5M2
 constexpr float kMinLogScale = -100.0f;                // token scales below 2^-100 count as 2^-100 in the reference
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kMaxSplits = 2 * kSplitSMs;
@@ -104,7 +104,7 @@ struct Smem {
     alignas(1024) uint8_t Qs[kBlocks][2 * R][128];       // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
     alignas(1024) uint8_t P[3 * NQ][kTileKeys][16];      // [term][query]: 16 rows of each key, no swizzle
     alignas(16) float sc[ST][kTileKeys];                 // the keys' token scales
-    int upos[ST][kTileKeys / kGroup];                    // position of each unit's first key, or one behind all where it has no page
+    int upos[ST][kTileKeys / kGroup];                    // position of each unit's first key; behind all without a page
     Tile tile[ST];
     alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     if (tid == 32 * kProducer) {
         for (int s = 0; s < ST; ++s)
             for (int c = 0; c < kBlocks; ++c) {
-                mbar_init(&sm.full[s][c], kByKeys && c == 0 ? 2 : 1);   // with the first part come the scales
-                mbar_init(&sm.empty[s][c], 1);
-            }
+            mbar_init(&sm.full[s][c], kByKeys && c == 0 ? 2 : 1);   // with the first part come the scales
+            mbar_init(&sm.empty[s][c], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], 4 * NQ);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (kByKeys && row4 >= 0) sc = __ldg(reinterpret_cast<const float4*>(sg.scales + row4 + ((4 * lane) & (unit - 1))));
         const uint32_t live = __ballot_sync(0xFFFFFFFFu, row >= 0);
-        const int first = sg.pos0 + sg.unit(v) * unit, last = first + unit - 1;
+        const int first = row >= 0 ? sg.pos0 + sg.unit(v) * unit : 0, last = first + unit - 1;
         const bool inside = row >= 0 && last < sg.end && last <= sg.imin && (first >= sg.lmax || (sg.own && last < p.n_sink));
         const int keys = min(kTileKeys, (sg.units - (t - sg.tile0) * upt) * unit);
         const Tile info = {sg.qa, sg.nq, (keys + 31) / 32, __popc(__ballot_sync(0xFFFFFFFFu, inside)) == upt, sg.end,
@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 if (lane == 0) sm.tile[st] = info;
             }
             const int upp = 32 >> ul;   // by keys: units of a part
-            const uint32_t bytes = kByKeys ? __popc(live & (((1u << upp) - 1u) << (c * upp))) * unit * kD : __popc(live) * unit * (c == 0 ? 128 + 4 : 128);
+            const uint32_t bytes = kByKeys ? __popc(live & (((1u << upp) - 1u) << (c * upp))) * unit * kD
+                                           : __popc(live) * unit * (c == 0 ? 128 + 4 : 128);
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], bytes);
             __syncwarp();
@@ -367,101 +368,105 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     if (warp == kProducer) {
         // ---- producer: an item's key lists and its tiles' copies.  It runs ahead of the others, so that an item's
         // chain of loads (positions, page table, rows) passes under the item before.
+        auto units_of = [&](int n) { return ((n - 1) >> ul) + 1; };   // n >= 1 keys; n + unit - 1 might not fit
+        auto tiles_of = [&](int u) { return ((u - 1) >> (7 - ul)) + 1; };
         int tile_no = 0;
         bool ok = true;
         for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
-        if (k >= 2) ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_empty[k & 1], (uint32_t)((k / 2 - 1) & 1)));
-        if (!ok) break;
-        const int block = it / args.splits, split = it - block * args.splits;
-        int f0, nq;
-        queries_of(block, f0, nq);
-        // lanes 0 .. NQ-1: a query each
-        int i = -1, low = 0, end = 0, pend = 0;
-        const int b = (f0 + min(lane, nq - 1)) / p.Q;
-        if (lane < nq) i = p.q_pos[f0 + lane];
-        if (lane < NQ) end = stored_end(p.own, b);
-        if (shared_prefix && lane == 0) pend = stored_end(p.prefix, 0);
-        if (i < 0) i = -1;
-        int64_t lw = p.window == 0x7FFFFFFF ? 0 : (int64_t)i - p.window + 1;
-        if (p.replay_start && lane < nq) lw = max(lw, (int64_t)p.replay_start[b]);
-        low = (int)max(lw, (int64_t)0);
-        Item<NQ>& item = sm.item[k & 1];
-        if (lane < NQ) {
-            item.qi[lane] = i;
-            item.qlow[lane] = low;
-        }
-        // Each lane's run of queries of one sequence: its extent and what its keys range over (every lane < nq alike).
-        const bool mine = lane < nq;
-        const int seq = mine ? b : -1;
-        int count = 0, head = 1, hi = 0, lo = 0x7FFFFFFF, rmin = 0x7FFFFFFF, rlow = 0, imax = -1, imin = 0x7FFFFFFF;
-#pragma unroll
-        for (int c = 0; c < NQ; ++c) {
-            const int oi = __shfl_sync(0xFFFFFFFFu, i, c), ol = __shfl_sync(0xFFFFFFFFu, low, c);
-            const bool same = __shfl_sync(0xFFFFFFFFu, seq, c) == seq;
-            if (c < nq) {
-                imax = max(imax, oi);
-                imin = min(imin, oi);
+            if (k >= 2) ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_empty[k & 1], (uint32_t)((k / 2 - 1) & 1)));
+            if (!ok) break;
+            const int block = it / args.splits, split = it - block * args.splits;
+            int f0, nq;
+            queries_of(block, f0, nq);
+            // lanes 0 .. NQ-1: a query each
+            int i = -1, low = 0, end = 0, pend = 0;
+            const int b = (f0 + min(lane, nq - 1)) / p.Q;
+            if (lane < nq) i = p.q_pos[f0 + lane];
+            if (lane < NQ) end = stored_end(p.own, b);
+            if (shared_prefix && lane == 0) pend = stored_end(p.prefix, 0);
+            if (i < 0) i = -1;
+            int64_t lw = p.window == 0x7FFFFFFF ? 0 : (int64_t)i - p.window + 1;
+            if (p.replay_start && lane < nq) lw = max(lw, (int64_t)p.replay_start[b]);
+            low = (int)max(lw, (int64_t)0);
+            Item<NQ>& item = sm.item[k & 1];
+            if (lane < NQ) {
+                item.qi[lane] = i;
+                item.qlow[lane] = low;
             }
-            if (c < nq && same) {
-                ++count;
-                if (c < lane) head = 0;
-                rmin = min(rmin, oi);
-                rlow = max(rlow, ol);
-                if (oi >= 0) {
-                    hi = max(hi, oi < end ? oi + 1 : end);
-                    lo = min(lo, ol);
-                }
-            }
-        }
-        int n = 0, tiles = 0;
-        if (shared_prefix) {
-            pend = __shfl_sync(0xFFFFFFFFu, pend, 0);
-            const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
-            if (e > 0) {
-                const int u = (e + unit - 1) >> ul;
-                if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
-                n = 1;
-                tiles = (u + upt - 1) >> (7 - ul);
-            }
-        }
-        {
-            // the sinks' units, then the window's from the first that holds no sink
-            const int base = p.own.pos0, ns = min(p.n_sink, hi) - base;
-            const int us = ns > 0 ? (ns + unit - 1) >> ul : 0;
-            const int ue = (hi - base + unit - 1) >> ul;
-            const int uw = max(us, lo > base ? (lo - base) >> ul : 0);
-            const int u = mine && head && hi > base ? us + max(0, ue - uw) : 0;
-            const int mytiles = (u + upt - 1) >> (7 - ul);
-            int at = n, tile0 = tiles;   // lists and tiles of the runs before this one
+            // Each lane's run of queries of one sequence: its extent and what its keys range over (every lane < nq alike).
+            const bool mine = lane < nq;
+            const int seq = mine ? b : -1;
+            int count = 0, head = 1, hi = 0, lo = 0x7FFFFFFF, rmin = 0x7FFFFFFF, rlow = 0, imax = -1, imin = 0x7FFFFFFF;
 #pragma unroll
             for (int c = 0; c < NQ; ++c) {
-                const int ot = __shfl_sync(0xFFFFFFFFu, mytiles, c);
-                if (c < lane) {
-                    at += ot > 0;
-                    tile0 += ot;
+                const int oi = __shfl_sync(0xFFFFFFFFu, i, c), ol = __shfl_sync(0xFFFFFFFFu, low, c);
+                const bool same = __shfl_sync(0xFFFFFFFFu, seq, c) == seq;
+                if (c < nq) {
+                    imax = max(imax, oi);
+                    imin = min(imin, oi);
                 }
-                n += ot > 0;
-                tiles += ot;
+                if (c < nq && same) {
+                    ++count;
+                    if (c < lane) head = 0;
+                    rmin = min(rmin, oi);
+                    rlow = max(rlow, ol);
+                    if (oi >= 0) {
+                        hi = max(hi, oi < end ? oi + 1 : end);
+                        lo = min(lo, ol);
+                    }
+                }
             }
-            if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow);
-        }
-        nseg = n;
-        const int each = tiles / args.splits, extra = tiles - each * args.splits;   // the first splits take one tile more
-        const int t0 = split * each + min(split, extra), nt = each + (split < extra);
-        if (lane == 0) {
-            item.tiles = nt;
-            item.part = it;
-        }
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(&sm.item_full[k & 1]);
-            if (it + gridDim.x < args.items) {   // the next item's queries on their way to L2
-                int g0, gn;
-                queries_of((it + gridDim.x) / args.splits, g0, gn);
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + (int64_t)g0 * kH * kD), "r"(gn * kH * kD * 2) : "memory");
+            int n = 0, tiles = 0;
+            if (shared_prefix) {
+                pend = __shfl_sync(0xFFFFFFFFu, pend, 0);
+                const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
+                if (e > 0) {
+                    const int u = units_of(e);
+                    if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
+                    n = 1;
+                    tiles = tiles_of(u);
+                }
             }
-        }
-        for (int t = 0; ok && t < nt; ++t, ++tile_no) ok = load_tile(t0 + t, tile_no);
+            {
+                // the sinks' units, then the window's from the first that holds no sink
+                const int base = p.own.pos0, ns = min(p.n_sink, hi) - base;
+                const int us = ns > 0 ? units_of(ns) : 0;
+                const int ue = hi > base ? units_of(hi - base) : 0;
+                const int uw = max(us, lo > base ? (lo - base) >> ul : 0);
+                const int u = mine && head && hi > base ? us + max(0, ue - uw) : 0;
+                const int mytiles = u > 0 ? tiles_of(u) : 0;
+                int at = n, tile0 = tiles;   // lists and tiles of the runs before this one
+#pragma unroll
+                for (int c = 0; c < NQ; ++c) {
+                    const int ot = __shfl_sync(0xFFFFFFFFu, mytiles, c);
+                    if (c < lane) {
+                        at += ot > 0;
+                        tile0 += ot;
+                    }
+                    n += ot > 0;
+                    tiles += ot;
+                }
+                if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow);
+            }
+            nseg = n;
+            const int each = tiles / args.splits, extra = tiles - each * args.splits;   // the first splits take one tile more
+            const int t0 = split * each + min(split, extra), nt = each + (split < extra);
+            if (lane == 0) {
+                item.tiles = nt;
+                item.part = it;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.item_full[k & 1]);
+                if (it + gridDim.x < args.items) {   // the next item's queries on their way to L2
+                    int g0, gn;
+                    queries_of((it + gridDim.x) / args.splits, g0, gn);
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + (int64_t)g0 * kH * kD),
+                                 "r"(gn * kH * kD * 2)
+                                 : "memory");
+                }
+            }
+            for (int t = 0; ok && t < nt; ++t, ++tile_no) ok = load_tile(t0 + t, tile_no);
         }
         if (!ok) {   // wind down: the copies in flight land before the CTA ends
             for (int n = max(0, tile_no - ST); n <= tile_no; ++n)
@@ -477,36 +482,36 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         bool ok = true;
         int n = 0;
         for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
-        ok = wait(&sm.item_full[k & 1], (uint32_t)((k >> 1) & 1)) && wait(&sm.q_full[k & 1], (uint32_t)((k >> 1) & 1));
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
-        for (; n < last && ok; ++n) {
-            const int st = n % ST;
-            if (n >= 2) ok = wait(&sm.s_free[n & 1], (uint32_t)((n / 2 - 1) & 1));
-            const int first_parts = kByKeys ? kBlocks : 1;
-#pragma unroll
-            for (int c = 0; c < first_parts; ++c) ok = ok && wait(&sm.full[st][c], (uint32_t)((n / ST) & 1));
+            ok = wait(&sm.item_full[k & 1], (uint32_t)((k >> 1) & 1)) && wait(&sm.q_full[k & 1], (uint32_t)((k >> 1) & 1));
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
-            const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
-            const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+            const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
+            for (; n < last && ok; ++n) {
+                const int st = n % ST;
+                if (n >= 2) ok = wait(&sm.s_free[n & 1], (uint32_t)((n / 2 - 1) & 1));
+                const int first_parts = kByKeys ? kBlocks : 1;
 #pragma unroll
-            for (int c = 0; c < kBlocks; ++c) {
-                if (!kByKeys && c > 0) {   // after a wait that ran out the products read what is there; S is not announced
-                    ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
-                    __syncwarp();
+                for (int c = 0; c < first_parts; ++c) ok = ok && wait(&sm.full[st][c], (uint32_t)((n / ST) & 1));
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
+                const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
+                const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+#pragma unroll
+                for (int c = 0; c < kBlocks; ++c) {
+                    if (!kByKeys && c > 0) {   // after a wait that ran out the products read what is there; S is not announced
+                        ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
+                        __syncwarp();
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
                 }
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
+                if (!kByKeys) ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                commit(lead, &sm.s_full[n & 1]);
             }
-            if (!kByKeys) ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            commit(lead, &sm.s_full[n & 1]);
-        }
-        if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
+            if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
         }
         if (!ok) {   // wind down: no product in flight when TMEM is freed
             commit(lead, &sm.wind_down[0]);
@@ -522,42 +527,43 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         bool ok = true;
         int n = 0;
         for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
-        ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_full[k & 1], (uint32_t)((k >> 1) & 1)));
-        const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
-        for (; n < last && ok; ++n) {
-            const int st = n % ST;
-            ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full, (uint32_t)(n & 1)));
-            if (!ok) break;
-            const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
-            const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
-            const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128);
-            tc_fence_after();
-            const uint64_t b = pd + qa * (2048 / 16);
-            const uint32_t d = td + kH * qa;
-            // Part i of the tile; its memory is free for a coming tile when its products are done.
-            auto parts = [&](auto product) {
+            ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_full[k & 1], (uint32_t)((k >> 1) & 1)));
+            const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
+            for (; n < last && ok; ++n) {
+                const int st = n % ST;
+                ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full, (uint32_t)(n & 1)));
+                if (!ok) break;
+                const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
+                const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
+                const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128);
+                tc_fence_after();
+                const uint64_t b = pd + qa * (2048 / 16);
+                const uint32_t d = td + kH * qa;
+                // Part i of the tile; its memory is free for a coming tile when its products are done.
+                auto parts = [&](auto product) {
 #pragma unroll
-                for (int i = 0; i < kBlocks; ++i) {
+                    for (int i = 0; i < kBlocks; ++i) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c = kByKeys ? j : i, s = kByKeys ? i : j;
-                        if (s < steps) product(c, a + (c * L::block + s * L::step) / 16, b + s * (512 / 16));
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = kByKeys ? j : i, s = kByKeys ? i : j;
+                            if (s < steps) product(c, a + (c * L::block + s * L::step) / 16, b + s * (512 / 16));
+                        }
+                        commit(lead, &sm.empty[st][i]);
                     }
-                    commit(lead, &sm.empty[st][i]);
-                }
-            };
-            if (kConcat && qn == NQ) {   // the three terms as one product
-                parts([&](int c, uint64_t as, uint64_t bs) { mma_f8(lead, d + c * kOCols, as, bs, idesc_pv(3 * R), 1); });
-            } else {
-                const uint32_t id = idesc_pv(kH * qn);
-                parts([&](int c, uint64_t as, uint64_t bs) {
+                };
+                if (kConcat && qn == NQ) {   // the three terms as one product
+                    parts([&](int c, uint64_t as, uint64_t bs) { mma_f8(lead, d + c * kOCols, as, bs, idesc_pv(3 * R), 1); });
+                } else {
+                    const uint32_t id = idesc_pv(kH * qn);
+                    parts([&](int c, uint64_t as, uint64_t bs) {
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), as, bs + x * NQ * (2048 / 16), id, 1);
-                });
+                        for (int x = 0; x < 3; ++x)
+                            mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), as, bs + x * NQ * (2048 / 16), id, 1);
+                    });
+                }
+                commit(lead, &sm.pv_done);
             }
-            commit(lead, &sm.pv_done);
-        }
-        if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
+            if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
         }
         if (!ok) {
             commit(lead, &sm.wind_down[1]);
@@ -579,224 +585,225 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         int f0 = 0, nq = 0, nt = 0, prev_f0 = 0, prev_nq = 0;
         int64_t part = 0;
         for (int k_item = 0, it = blockIdx.x;; ++k_item, it += gridDim.x) {
-        const bool have = it < args.items;
-        float(&rowf)[R] = sm.rowf[k_item & 1];
-        prev_f0 = f0;
-        prev_nq = nq;
-        if (have) {
-        // Q: four rows (heads) of this query in each warp, 16 channels per lane -> E4M3 hi and lo, each row scaled so that
-        // its largest is in [2^7, 2^8)
-        queries_of(it / args.splits, f0, nq);
-        uint4 v[4][2];
+            const bool have = it < args.items;
+            float(&rowf)[R] = sm.rowf[k_item & 1];
+            prev_f0 = f0;
+            prev_nq = nq;
+            if (have) {
+                // Q: four rows (heads) of this query in each warp, 16 channels per lane -> E4M3 hi and lo, each row scaled
+                // so that its largest is in [2^7, 2^8)
+                queries_of(it / args.splits, f0, nq);
+                uint4 v[4][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-            if (wg < nq) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(f0 + wg) * kH + quarter + 4 * k) * kD) + 2 * lane;
-                v[k][0] = __ldg(src);
-                v[k][1] = __ldg(src + 1);
-            }
-        }
-        const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
-        if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
-        float top[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top[k] = redux_max(top[k]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int h = quarter + 4 * k, r = kH * wg + h;
-            const int e = max((int)((__float_as_uint(top[k]) >> 23) & 0xFFu) - 127 - 7, -120);
-            const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4& vv = v[k][j >> 1];
-                const uint32_t w0 = (j & 1) ? vv.z : vv.x, w1 = (j & 1) ? vv.w : vv.y;
-                const float x[4] = {__uint_as_float(w0 << 16) * mul, __uint_as_float(w0 & 0xFFFF0000u) * mul,
-                                    __uint_as_float(w1 << 16) * mul, __uint_as_float(w1 & 0xFFFF0000u) * mul};
-                uint16_t a, b2;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1]), "f"(x[0]));
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3]), "f"(x[2]));
-                hi[j] = (uint32_t)a | ((uint32_t)b2 << 16);
-                float y[4];
-                e4m3x4_to_f32(hi[j], y);
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1] - y[1]), "f"(x[0] - y[0]));
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3] - y[3]), "f"(x[2] - y[2]));
-                lo[j] = (uint32_t)a | ((uint32_t)b2 << 16);
-            }
-            const int rh = 32 * wg + h, rl = rh + 16, chunk = lane & 7;
-            *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (lane == 0)
-                rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full[k_item & 1]);
-        }
-        if (k_item > 0) {
-        // ---- the output of the item before ----
-        wg_bar(wg);
-        if (key < kH) {
-            const int r = kH * wg + key;
-            const float sum = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]), ref = sm.mref[r];
-            if (args.splits > 1) {
-                float* ml = args.part_ml + (part * R + r) * 2;
-                *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
-            } else if (p.lse && wg < prev_nq) {
-                p.lse[(int64_t)(prev_f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-            }
-            sm.mref[r] = -INFINITY;   // for the next item
-            sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
-        }
-        wg_bar(wg);
-        if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
-        tc_fence_after();
-        float fac[kH];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 f = row4(sm.fac, j);
-            fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
-        }
-        float* po = args.part_o + (part * R + kH * wg) * kD;
-        // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
-        uint16_t* out = p.out + ((int64_t)(prev_f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            uint32_t o[kTerms][16];
-#pragma unroll
-            for (int y = 0; y < kTerms; ++y) tmem_ld_32x32b_x16(ocol(b, y), o[y]);
-            tmem_ld_wait();
-            float y[kH];
-#pragma unroll
-            for (int h = 0; h < kH; ++h) {
-                y[h] = __uint_as_float(o[0][h]);
-#pragma unroll
-                for (int x = 1; x < kTerms; ++x) y[h] += __uint_as_float(o[x][h]);
-                y[h] *= fac[h];
-            }
-            if (args.splits > 1) {
-#pragma unroll
-                for (int h = 0; h < kH; ++h) po[h * kD + 128 * b + key] = y[h];
-            } else if (wg < prev_nq) {
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    const uint32_t own = pack_bf16(y[h], y[h + 8]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
-                    *reinterpret_cast<uint32_t*>(out + h * kD + 128 * b) =
-                        (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+                for (int k = 0; k < 4; ++k) {
+                    v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+                    if (wg < nq) {
+                        const int64_t row = (int64_t)(f0 + wg) * kH + quarter + 4 * k;
+                        const uint4* src = reinterpret_cast<const uint4*>(p.q + row * kD) + 2 * lane;
+                        v[k][0] = __ldg(src);
+                        v[k][1] = __ldg(src + 1);
+                    }
                 }
-            }
-        }
-        tc_fence_before();
-        wg_bar(wg);   // fac and mref are free
-        }
-        if (!have) break;
-
-        const Item<NQ>& item = sm.item[k_item & 1];
-        const int qi = item.qi[wg], qlow = item.qlow[wg];
-        nt = item.tiles;
-        part = item.part;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.item_empty[k_item & 1]);
-        {
-            uint32_t zero[16] = {};
+                const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
+                if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
+                float top[4];
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b)
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
 #pragma unroll
-                for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
-            tmem_st_wait();
-        }
-        wg_bar(wg);   // rowf of the whole query
-        float l[kH];
+                for (int k = 0; k < 4; ++k) top[k] = redux_max(top[k]);
 #pragma unroll
-        for (int h = 0; h < kH; ++h) l[h] = 0.0f;
-
-        // After a wait that ran out the loop goes on with what is there: every thread passes every named barrier.
-        for (int i = 0; i < nt; ++i, ++n) {
-            const int st = n % ST;
-            bool ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
-            const Tile tile = sm.tile[st];
-            const bool active = wg >= tile.qa && wg < tile.qa + tile.nq;   // this tile's products cover this query
-            bool seen = active;
-            if (!tile.interior) {
-                const int pos = sm.upos[st][ku] + ko;
-                seen = active && pos < tile.end && pos <= qi && (pos >= qlow || pos < tile.sink);
-            }
-            const float ts = seen ? sm.sc[st][key] : 0.0f;
-            bool dirty = false;
-            ok = wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1)) && ok;
-            tc_fence_after();
-            if (active) {
-                const float lsc = fmaxf(__log2f(ts), kMinLogScale);
-                float x[kH];   // logits in log2 units less the rows' references
-                auto sums = [&](uint32_t (&u)[32]) {   // hi in u[0 .. 15], lo in u[16 .. 31]
-                    tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * R + 32 * wg, u);
-                    tmem_ld_wait();
-                };
-                bool move = i == 0;
-                if (i > 0) {
-                    uint32_t u[32];
-                    sums(u);
-                    float top = -INFINITY;
+                for (int k = 0; k < 4; ++k) {
+                    const int h = quarter + 4 * k, r = kH * wg + h;
+                    const int e = max((int)((__float_as_uint(top[k]) >> 23) & 0xFFu) - 127 - 7, -120);
+                    const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 f4 = row4(rowf, j), m4 = row4(sm.mref, j);
-                        const float f[4] = {f4.x, f4.y, f4.z, f4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
+                        const uint4& vv = v[k][j >> 1];
+                        const uint32_t w0 = (j & 1) ? vv.z : vv.x, w1 = (j & 1) ? vv.w : vv.y;
+                        const float x[4] = {__uint_as_float(w0 << 16) * mul, __uint_as_float(w0 & 0xFFFF0000u) * mul,
+                                            __uint_as_float(w1 << 16) * mul, __uint_as_float(w1 & 0xFFFF0000u) * mul};
+                        uint16_t a, b2;
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1]), "f"(x[0]));
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3]), "f"(x[2]));
+                        hi[j] = (uint32_t)a | ((uint32_t)b2 << 16);
+                        float y[4];
+                        e4m3x4_to_f32(hi[j], y);
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x[1] - y[1]), "f"(x[0] - y[0]));
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3] - y[3]), "f"(x[2] - y[2]));
+                        lo[j] = (uint32_t)a | ((uint32_t)b2 << 16);
+                    }
+                    const int rh = 32 * wg + h, rl = rh + 16, chunk = lane & 7;
+                    *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (lane == 0)
+                        rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_full[k_item & 1]);
+            }
+            if (k_item > 0) {
+                // ---- the output of the item before ----
+                wg_bar(wg);
+                if (key < kH) {
+                    const int r = kH * wg + key;
+                    const float sum = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]), ref = sm.mref[r];
+                    if (args.splits > 1) {
+                        float* ml = args.part_ml + (part * R + r) * 2;
+                        *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
+                    } else if (p.lse && wg < prev_nq) {
+                        p.lse[(int64_t)(prev_f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                    }
+                    sm.mref[r] = -INFINITY;   // for the next item
+                    sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
+                }
+                wg_bar(wg);
+                if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+                tc_fence_after();
+                float fac[kH];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int h = 4 * j + c;
-                            x[h] = fmaf(__uint_as_float(u[h]) + __uint_as_float(u[16 + h]), ts * f[c], -m[c]);
-                            top = fmaxf(top, x[h]);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 f = row4(sm.fac, j);
+                    fac[4 * j] = f.x, fac[4 * j + 1] = f.y, fac[4 * j + 2] = f.z, fac[4 * j + 3] = f.w;
+                }
+                float* po = args.part_o + (part * R + kH * wg) * kD;
+                // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
+                uint16_t* out = p.out + ((int64_t)(prev_f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    uint32_t o[kTerms][16];
+#pragma unroll
+                    for (int y = 0; y < kTerms; ++y) tmem_ld_32x32b_x16(ocol(b, y), o[y]);
+                    tmem_ld_wait();
+                    float y[kH];
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) {
+                        y[h] = __uint_as_float(o[0][h]);
+#pragma unroll
+                        for (int x = 1; x < kTerms; ++x) y[h] += __uint_as_float(o[x][h]);
+                        y[h] *= fac[h];
+                    }
+                    if (args.splits > 1) {
+#pragma unroll
+                        for (int h = 0; h < kH; ++h) po[h * kD + 128 * b + key] = y[h];
+                    } else if (wg < prev_nq) {
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            const uint32_t own = pack_bf16(y[h], y[h + 8]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+                            *reinterpret_cast<uint32_t*>(out + h * kD + 128 * b) =
+                                (lane & 1) ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
                         }
                     }
-                    dirty = !seen && x[0] != x[0];
-                    move = wg_any(wg, seen && top + lsc > kHeadroom);
                 }
-                // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
-                if (__builtin_expect(move, 0)) {
-                    // here each product is rounded for itself, in the maximum as below: huge logits meet it exactly
-                    float mx[kH];
-                    {
+                tc_fence_before();
+                wg_bar(wg);   // fac and mref are free
+            }
+            if (!have) break;
+
+            const Item<NQ>& item = sm.item[k_item & 1];
+            const int qi = item.qi[wg], qlow = item.qlow[wg];
+            nt = item.tiles;
+            part = item.part;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.item_empty[k_item & 1]);
+            {
+                uint32_t zero[16] = {};
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                    for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
+                tmem_st_wait();
+            }
+            wg_bar(wg);   // rowf of the whole query
+            float l[kH];
+#pragma unroll
+            for (int h = 0; h < kH; ++h) l[h] = 0.0f;
+
+            // After a wait that ran out the loop goes on with what is there: every thread passes every named barrier.
+            for (int i = 0; i < nt; ++i, ++n) {
+                const int st = n % ST;
+                bool ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
+                const Tile tile = sm.tile[st];
+                const bool active = wg >= tile.qa && wg < tile.qa + tile.nq;   // this tile's products cover this query
+                bool seen = active;
+                if (!tile.interior) {
+                    const int pos = sm.upos[st][ku] + ko;
+                    seen = active && pos < tile.end && pos <= qi && (pos >= qlow || pos < tile.sink);
+                }
+                const float ts = seen ? sm.sc[st][key] : 0.0f;
+                bool dirty = false;
+                ok = wait(&sm.s_full[n & 1], (uint32_t)((n >> 1) & 1)) && ok;
+                tc_fence_after();
+                if (active) {
+                    const float lsc = fmaxf(__log2f(ts), kMinLogScale);
+                    float x[kH];   // logits in log2 units less the rows' references
+                    auto sums = [&](uint32_t (&u)[32]) {   // hi in u[0 .. 15], lo in u[16 .. 31]
+                        tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * R + 32 * wg, u);
+                        tmem_ld_wait();
+                    };
+                    bool move = i == 0;
+                    if (i > 0) {
                         uint32_t u[32];
                         sums(u);
+                        float top = -INFINITY;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float4 f4 = row4(rowf, j);
-                            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+                            const float4 f4 = row4(rowf, j), m4 = row4(sm.mref, j);
+                            const float f[4] = {f4.x, f4.y, f4.z, f4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
                                 const int h = 4 * j + c;
-                                x[h] = __fmul_rn(__fmul_rn(__uint_as_float(u[h]) + __uint_as_float(u[16 + h]), ts), f[c]);
+                                x[h] = fmaf(__uint_as_float(u[h]) + __uint_as_float(u[16 + h]), ts * f[c], -m[c]);
+                                top = fmaxf(top, x[h]);
                             }
                         }
+                        dirty = !seen && x[0] != x[0];
+                        move = wg_any(wg, seen && top + lsc > kHeadroom);
                     }
-                    dirty = !seen && x[0] != x[0];
+                    // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
+                    if (__builtin_expect(move, 0)) {
+                        // here each product is rounded for itself, in the maximum as below: huge logits meet it exactly
+                        float mx[kH];
+                        {
+                            uint32_t u[32];
+                            sums(u);
 #pragma unroll
-                    for (int h = 0; h < kH; ++h) mx[h] = redux_max(seen ? x[h] + lsc : -INFINITY);
-                    if (lane == 0) {
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 f4 = row4(rowf, j);
+                                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<float4*>(&sm.wmax[quarter][kH * wg + 4 * j]) =
-                                make_float4(mx[4 * j], mx[4 * j + 1], mx[4 * j + 2], mx[4 * j + 3]);
-                    }
-                    wg_bar(wg);
-                    if (key < kH) {
-                        const int r = kH * wg + key;
-                        const float m = fmaxf(fmaxf(sm.wmax[0][r], sm.wmax[1][r]), fmaxf(sm.wmax[2][r], sm.wmax[3][r]));
-                        const float old = sm.mref[r];
-                        sm.fac[r] = m > old ? (old == -INFINITY ? 0.0f : ex2(old - m)) : 1.0f;
-                        sm.mref[r] = fmaxf(m, old);
-                    }
-                    wg_bar(wg);
-                    if (i > 0) {
-                        wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
-                        tc_fence_after();
+                                for (int c = 0; c < 4; ++c) {
+                                    const int h = 4 * j + c;
+                                    x[h] = __fmul_rn(__fmul_rn(__uint_as_float(u[h]) + __uint_as_float(u[16 + h]), ts), f[c]);
+                                }
+                            }
+                        }
+                        dirty = !seen && x[0] != x[0];
+#pragma unroll
+                        for (int h = 0; h < kH; ++h) mx[h] = redux_max(seen ? x[h] + lsc : -INFINITY);
+                        if (lane == 0) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<float4*>(&sm.wmax[quarter][kH * wg + 4 * j]) =
+                                    make_float4(mx[4 * j], mx[4 * j + 1], mx[4 * j + 2], mx[4 * j + 3]);
+                        }
+                        wg_bar(wg);
+                        if (key < kH) {
+                            const int r = kH * wg + key;
+                            const float m = fmaxf(fmaxf(sm.wmax[0][r], sm.wmax[1][r]), fmaxf(sm.wmax[2][r], sm.wmax[3][r]));
+                            const float old = sm.mref[r];
+                            sm.fac[r] = m > old ? (old == -INFINITY ? 0.0f : ex2(old - m)) : 1.0f;
+                            sm.mref[r] = fmaxf(m, old);
+                        }
+                        wg_bar(wg);
+                        if (i > 0) {
+                            wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int b = 0; b < kBlocks; ++b)
+                            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll 1
-                            for (int y = 0; y < kTerms; ++y) {
+                                for (int y = 0; y < kTerms; ++y) {
                                 uint32_t o[16];
                                 tmem_ld_32x32b_x16(ocol(b, y), o);
                                 tmem_ld_wait();
@@ -804,80 +811,80 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                                 for (int h = 0; h < kH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sm.fac[kH * wg + h]);
                                 tmem_st_x16(ocol(b, y), o);
                             }
-                        tmem_st_wait();
-                    }
-                    if (i > 0) {
+                            tmem_st_wait();
+                        }
+                        if (i > 0) {
 #pragma unroll
-                        for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
+                            for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 m = row4(sm.mref, j);
+                            x[4 * j] -= m.x, x[4 * j + 1] -= m.y, x[4 * j + 2] -= m.z, x[4 * j + 3] -= m.w;
+                        }
                     }
+                    if (!tile.interior) {
+#pragma unroll
+                        for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
+                    const float tp = ts * kPScale;
+                    uint32_t w[3][4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float4 m = row4(sm.mref, j);
-                        x[4 * j] -= m.x, x[4 * j + 1] -= m.y, x[4 * j + 2] -= m.z, x[4 * j + 3] -= m.w;
-                    }
-                }
-                if (!tile.interior) {
+                        float e[4];
 #pragma unroll
-                    for (int h = 0; h < kH; ++h) x[h] = seen ? x[h] : -INFINITY;
+                        for (int i = 0; i < 4; ++i) {
+                            e[i] = ex2(x[4 * j + i]);
+                            l[4 * j + i] += e[i];
+                        }
+                        uint32_t h0, m0, l0, h1, m1, l1;
+                        split_e5m2(pack_f16(e[0] * tp, e[1] * tp), h0, m0, l0);
+                        split_e5m2(pack_f16(e[2] * tp, e[3] * tp), h1, m1, l1);
+                        w[0][j] = __byte_perm(h0, h1, 0x7531);
+                        w[1][j] = __byte_perm(m0, m1, 0x7531);
+                        w[2][j] = __byte_perm(l0, l1, 0x7531);
+                    }
+                    if (n > 0) ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;   // P is free when the last tile's products are done
+#pragma unroll
+                    for (int y = 0; y < 3; ++y)
+                        *reinterpret_cast<uint4*>(&sm.P[y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+                } else if (n > 0) {
+                    // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
+                    ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;
                 }
+                if (!active && lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
+                if (dirty && ok) {   // S of this tile is done: only P K still reads the row
+                    for (int b = wg - tile.qa; b < kBlocks; b += tile.nq)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(&sm.K[st][(key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7)]) =
+                                make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
-                const float tp = ts * kPScale;
-                uint32_t w[3][4];
+                if (ok) mbar_arrive(&sm.p_full);
+            }
+            // ---- row sums over the 128 threads ----
+            {
+                // halving exchange: after step o a lane holds the sums over lane pairs of half as many rows
+                float v[kH];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float e[4];
+                for (int h = 0; h < kH; ++h) v[h] = l[h];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        e[i] = ex2(x[4 * j + i]);
-                        l[4 * j + i] += e[i];
+                for (int o = 8; o > 0; o >>= 1) {
+                    const bool up = (lane & o) != 0;
+#pragma unroll
+                    for (int h = 0; h < o; ++h) {
+                        const float keep = up ? v[h + o] : v[h], give = up ? v[h] : v[h + o];
+                        v[h] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
                     }
-                    uint32_t h0, m0, l0, h1, m1, l1;
-                    split_e5m2(pack_f16(e[0] * tp, e[1] * tp), h0, m0, l0);
-                    split_e5m2(pack_f16(e[2] * tp, e[3] * tp), h1, m1, l1);
-                    w[0][j] = __byte_perm(h0, h1, 0x7531);
-                    w[1][j] = __byte_perm(m0, m1, 0x7531);
-                    w[2][j] = __byte_perm(l0, l1, 0x7531);
                 }
-                if (n > 0) ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;   // P is free when the last tile's products are done
-#pragma unroll
-                for (int y = 0; y < 3; ++y)
-                    *reinterpret_cast<uint4*>(&sm.P[y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
-            } else if (n > 0) {
-                // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
-                ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;
+                v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);   // lane i: row i & 15
+                if (lane < kH) sm.lsum[quarter][kH * wg + lane] = v[0];
             }
-            if (!active && lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
-            if (dirty && ok) {   // S of this tile is done: only P K still reads the row
-                for (int b = wg - tile.qa; b < kBlocks; b += tile.nq)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(&sm.K[st][(key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7)]) =
-                            make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            if (ok) mbar_arrive(&sm.p_full);
-        }
-        // ---- row sums over the 128 threads ----
-        {
-            // halving exchange: after step o a lane holds the sums over lane pairs of half as many rows
-            float v[kH];
-#pragma unroll
-            for (int h = 0; h < kH; ++h) v[h] = l[h];
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
-                const bool up = (lane & o) != 0;
-#pragma unroll
-                for (int h = 0; h < o; ++h) {
-                    const float keep = up ? v[h + o] : v[h], give = up ? v[h] : v[h + o];
-                    v[h] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-                }
-            }
-            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);   // lane i: row i & 15
-            if (lane < kH) sm.lsum[quarter][kH * wg + lane] = v[0];
-        }
         }
     }
     __syncthreads();

@@ -273,6 +273,72 @@ def test_prefix_equals_each_sequence_alone(csa):
     check(*run_window(csa, whole, q, q_pos, 1 << 30, 0), ref)
 
 
+@pytest.mark.parametrize("B,Q,window,sink,page", [(400, 1, 50, 3, 16), (310, 2, 20, 0, 32), (3, 250, 24, 2, 64), (160, 3, 5, 1, 8)])
+def test_more_items_than_the_gpu_holds(csa, B, Q, window, sink, page):
+    """CTAs walk over several items each, some of them without a query or a token."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(0, 2 * Q + 60, B)]
+    lens[B // 3] = 0
+    cache = Cache(B + Q, lens, page)
+    q, q_pos = queries(B, B, Q), tail_positions(lens, Q)
+    out, lse = run_window(csa, cache, q, q_pos, window, sink)
+    check(out, lse, reference(q, q_pos, [(cache, True)], window, sink))
+
+
+@pytest.mark.parametrize("Q", [1, 3, 2, 20])
+def test_window_table_that_starts_later(csa, Q):
+    """pos0 > 0: the table's first slot is a later token; sinks count by position."""
+    lens = [300, 41]
+    cache = Cache(17, lens, 16, pos0=1000)
+    q, q_pos = queries(8, 2, Q), tail_positions(lens, Q) + 1000
+    for window, sink in ((70, 0), (70, 1013), (16, 5)):
+        out, lse = run_window(csa, cache, q, q_pos, window, sink)
+        check(out, lse, reference(q, q_pos, [(cache, True)], window, sink))
+
+
+@pytest.mark.parametrize("page_prefix,page_own", [(64, 16), (8, 128), (256, 64), (24, 40)])
+def test_prefix_pages_of_another_size(csa, page_prefix, page_own):
+    prefix, mine = Cache(51, [777], page_prefix), Cache(52, [130, 1, 64, 9, 300], page_own, pos0=777)
+    q, q_pos = queries(7, 5, 1), np.array([[777 + n - 1] for n in (130, 1, 64, 9, 300)], np.int32)
+    check(*run_prefix(csa, prefix, mine, q, q_pos), reference(q, q_pos, [(prefix, False), (mine, True)]))
+
+
+def test_prefix_without_own_tokens_or_prefix(csa):
+    """An empty prefix, sequences of no token, and both."""
+    q_pos = np.array([[5], [0], [9], [3]], np.int32)
+    q = queries(12, 4, 1)
+    for n, own in ((0, [6, 1, 10, 0]), (7, [0, 0, 3, 0]), (0, [0, 0, 0, 0])):
+        prefix, mine = Cache(61, [n], 16), Cache(62, own, 16, pos0=n)
+        check(*run_prefix(csa, prefix, mine, q, q_pos), reference(q, q_pos, [(prefix, False), (mine, True)]))
+
+
+def test_a_table_wider_than_memory(csa):
+    """A table that could name 2^31 - 64 tokens: the sizes stay within 32 bits (the pages it names are few)."""
+    width = (1 << 31) // 4096 - 1
+    small = Cache(63, [4096 + 50], 4096, n_pages=3)
+    kv, sc = torch.from_numpy(small.kv).cuda(), torch.from_numpy(small.kv_sc).cuda()
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    last = width * 4096   # positions last - 4096 - 50 ..: the table's end
+    table[0, width - 2:] = torch.from_numpy(small.table[0]).cuda()
+    pages = csa.Pages.of(kv, sc, table, torch.full((1,), last, dtype=torch.int32, device="cuda"))
+    shifted = Cache(63, [4096 + 50], 4096, n_pages=3, pos0=last - 8192)
+    shifted.n_tokens[0] = 8192
+    q, q_pos = queries(14, 1, 2), np.array([[last - 1, last - 4000]], np.int32)
+    out, lse = run_window(csa, pages, q, q_pos, 300, 0)
+    check(out, lse, reference(q, q_pos, [(shifted, True)], 300, 0))
+
+
+@pytest.mark.parametrize("Q", [1, 4])
+def test_zero_queries_do_not_hide_masked_nan(csa, Q):
+    """Heads of zeros beside NaN slots: zero times NaN must not reach the output."""
+    lens = [200]
+    cache = Cache(64, lens, 16)
+    q, q_pos = queries(15, 1, Q), tail_positions(lens, Q)
+    q[:, :, :5] = 0
+    cache.poison_dead({cache.row(0, j) for i in q_pos[0] for j in visible(cache, 0, int(i), 30, 2)})
+    check(*run_window(csa, cache, q, q_pos, 30, 2), reference(q, q_pos, [(cache, True)], 30, 2))
+
+
 # ---- as they are used --------------------------------------------------------------------------
 
 def test_decode_run(csa):
