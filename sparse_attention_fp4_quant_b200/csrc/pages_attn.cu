@@ -637,7 +637,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     if (lane == 0)
-                        rowf[r] = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
+                        rowf[r] = top[k] < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f)
+                                                    : __uint_as_float(0x7FC00000u);   // an infinite query gives NaN
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -653,10 +654,10 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                         float* ml = args.part_ml + (part * R + r) * 2;
                         *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
                     } else if (p.lse && wg < prev_nq) {
-                        p.lse[(int64_t)(prev_f0 + wg) * kH + key] = sum > 0.0f ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                        p.lse[(int64_t)(prev_f0 + wg) * kH + key] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
                     }
                     sm.mref[r] = -INFINITY;   // for the next item
-                    sm.fac[r] = (args.splits > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f) * (1.0f / kPScale);
+                    sm.fac[r] = (args.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum) * (1.0f / kPScale);
                 }
                 wg_bar(wg);
                 if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
@@ -956,10 +957,10 @@ __global__ void __launch_bounds__(128 * kGroups) pages_merge_kernel(const __grid
             o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
         }
     }
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     *reinterpret_cast<uint2*>(p.out + (int64_t)blockIdx.x * kD + 4 * col) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.lse && tid == 0) p.lse[blockIdx.x] = L > 0.0f ? (Mu + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    if (p.lse && tid == 0) p.lse[blockIdx.x] = L == 0.0f ? -INFINITY : (Mu + log2f(L)) * 0.6931471805599453f;
 }
 
 // ---- host ----------------------------------------------------------------------------------

@@ -339,6 +339,22 @@ def test_zero_queries_do_not_hide_masked_nan(csa, Q):
     check(*run_window(csa, cache, q, q_pos, 30, 2), reference(q, q_pos, [(cache, True)], 30, 2))
 
 
+@pytest.mark.parametrize("Q,n", [(1, 200), (1, 3000), (4, 200), (9, 700)])
+def test_a_query_of_nan_or_infinity_keeps_to_itself(csa, Q, n):
+    """NaN and infinite heads give NaN; every other head's result is bit-identical to the clean call's."""
+    cache = Cache(65, [n], 64)
+    q, q_pos = queries(16, 1, Q), tail_positions([n], Q)
+    clean = run_window(csa, cache, q, q_pos, 1 << 30, 0)
+    bad = q.clone()
+    bad[0, 0, 3, 17], bad[0, Q - 1, 9, 500] = float("nan"), float("inf")
+    out, lse = run_window(csa, cache, bad, q_pos, 1 << 30, 0)
+    hit = torch.zeros((1, Q, H), dtype=torch.bool)
+    hit[0, 0, 3] = hit[0, Q - 1, 9] = True
+    hit = hit.cuda()
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
 # ---- as they are used --------------------------------------------------------------------------
 
 def test_decode_run(csa):
