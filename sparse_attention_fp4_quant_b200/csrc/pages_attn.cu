@@ -176,6 +176,12 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 
+// The largest |bf16| of eight, by bits (the order of their integers puts infinity and NaN on top), one per half.
+__device__ __forceinline__ uint32_t bf16x8_topbits(uint4 v) {
+    const uint32_t m = 0x7FFF7FFFu;
+    return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+}
+
 __device__ __forceinline__ float redux_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -606,15 +612,18 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 }
                 const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
                 if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
-                float top[4];
+                uint32_t top[4];   // bits of the row's largest |bf16|; from 0x7F80 on the row holds an infinity or NaN
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = fmaxf(bf16x8_maxabs(v[k][0]), bf16x8_maxabs(v[k][1]));
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = redux_max(top[k]);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t t = __vmaxu2(bf16x8_topbits(v[k][0]), bf16x8_topbits(v[k][1]));
+                    top[k] = __reduce_max_sync(0xFFFFFFFFu, max(t & 0xFFFFu, t >> 16));
+                    // such a row enters the products as zeros and gets its NaN by rowf: S is NaN only where K is
+                    if (top[k] >= 0x7F80u) v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int h = quarter + 4 * k, r = kH * wg + h;
-                    const int e = max((int)((__float_as_uint(top[k]) >> 23) & 0xFFu) - 127 - 7, -120);
+                    const int e = max((int)(top[k] >> 7) - 127 - 7, -120);
                     const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
                     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -633,12 +642,11 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3] - y[3]), "f"(x[2] - y[2]));
                         lo[j] = (uint32_t)a | ((uint32_t)b2 << 16);
                     }
-                    const int rh = 32 * wg + h, rl = rh + 16, chunk = lane & 7;
-                    *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][(chunk ^ (rh & 7)) << 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][(chunk ^ (rl & 7)) << 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    if (lane == 0)
-                        rowf[r] = top[k] < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f)
-                                                    : __uint_as_float(0x7FC00000u);   // an infinite query gives NaN
+                    const int rh = 32 * wg + h, rl = rh + 16, at = ((lane & 7) ^ (rh & 7)) << 4;   // rl & 7 is the same
+                    *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][at]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][at]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const float scale = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
+                    if (lane == 0) rowf[r] = top[k] < 0x7F80u ? scale : __uint_as_float(0x7FC00000u);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -742,6 +750,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     auto sums = [&](uint32_t (&u)[32]) {   // hi in u[0 .. 15], lo in u[16 .. 31]
                         tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * R + 32 * wg, u);
                         tmem_ld_wait();
+                        dirty = !seen && isnan(__uint_as_float(u[0]));
                     };
                     bool move = i == 0;
                     if (i > 0) {
@@ -759,7 +768,6 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                                 top = fmaxf(top, x[h]);
                             }
                         }
-                        dirty = !seen && x[0] != x[0];
                         move = wg_any(wg, seen && top + lsc > kHeadroom);
                     }
                     // A weight beyond the headroom (or a row's first keys, against a reference of -inf): move the references.
@@ -780,7 +788,6 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                                 }
                             }
                         }
-                        dirty = !seen && x[0] != x[0];
 #pragma unroll
                         for (int h = 0; h < kH; ++h) mx[h] = redux_max(seen ? x[h] + lsc : -INFINITY);
                         if (lane == 0) {

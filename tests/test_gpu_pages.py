@@ -355,6 +355,25 @@ def test_a_query_of_nan_or_infinity_keeps_to_itself(csa, Q, n):
     assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("ps", [16, 64])
+def test_keys_that_a_nan_query_does_not_see(csa, ps, value):
+    """A first query whose every head holds NaN or infinity leaves the keys behind it, which it does not see, to the
+    queries of its tile that do."""
+    cache = Cache(66, [300], ps)
+    q, q_pos = queries(17, 1, 8), np.array([[100, 299, 298, 101, 40, 41, 42, 299]], np.int32)
+    clean = run_window(csa, cache, q, q_pos, 1 << 30, 0)
+    bad = q.clone()
+    bad[0, 0, :, 7] = value
+    bad[0, 4, 0, 511] = value
+    out, lse = run_window(csa, cache, bad, q_pos, 1 << 30, 0)
+    assert out[0, 0].isnan().all() and out[0, 4, 0].isnan().all() and lse[0, 0].isnan().all()
+    keep = torch.ones((1, 8, H), dtype=torch.bool)
+    keep[0, 0], keep[0, 4, 0] = False, False
+    keep = keep.cuda()
+    assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
 # ---- as they are used --------------------------------------------------------------------------
 
 def test_decode_run(csa):
