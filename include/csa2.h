@@ -487,7 +487,7 @@ CSA2_API csa2_status csa2_pages_append(const void* x, int64_t x_stride, int64_t 
  *   replay_start  device int32 [B] or NULL
  *   ws, ws_bytes  device workspace of csa2_workspace_bytes(CSA2_OP_WINDOW_ATTN, ...), 16-byte aligned;
  *                 its contents do not matter.  Calls that may run at the same time need their own.
- *   Numerics: fp32 logits, softmax statistics and sums; the query is held to 2^-18 of a head's
+ *   Numerics: fp32 logits, softmax statistics and sums; the query is held to 2^-17 of a head's
  *                 largest element, a weight times its token's scale to 2^-9 of itself, or 2^-29 of the
  *                 row's largest where that is more.
  *   flag          device int32, zero before first use, or NULL: set to 1 when a device-side

@@ -9,8 +9,8 @@
 // unconverted: the same shared-memory tile is read K-major for S and channel-major for O.
 // What the other operand loses is bounded:
 //   Q   a bf16 has 8 significant bits, an E4M3 pair hi + lo holds 4 + 4: exact, apart from
-//       elements 2^-10 below the row's largest (each row scaled by its own power of two),
-//       which are held to 2^-18 of it.  hi and lo are separate columns of S, added in fp32.
+//       elements below 2^-9 of the row's largest (each row scaled by its own power of two),
+//       which are held to 2^-17 of it.  hi and lo are separate columns of S, added in fp32.
 //   P   each weight times its token scale, as f16 with 2^12 of headroom below the maximum,
 //       split in three E5M2 terms (f16's exponent range): at least 9 significant bits; what is
 //       smaller than 2^-26 of the row's largest is held to 2^-29 of it (E5M2's smallest step).
