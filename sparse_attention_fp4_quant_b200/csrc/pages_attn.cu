@@ -22,6 +22,8 @@
 // S is NaN as well, so its thread finds out for nothing, and zeroes the row before P K.
 #include <cuda.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "tc.cuh"
 
@@ -54,6 +56,7 @@ struct Seg {
     int pos0, end;  // position of slot 0, and of the first slot behind the stored tokens
     int imin, lmax;  // every query of the list sees the stored tokens in [lmax, imin]
     int page_size, n_pages;
+    uint32_t recip;         // floor((2^32 - 1) / units of a page)
     const int32_t* table;   // the sequence's row
     const float* scales;
 
@@ -61,8 +64,8 @@ struct Seg {
 };
 
 __device__ __forceinline__ Seg make_seg(const csa2_pages& pg, int own, int b, int tile0, int units, int sink, int delta,
-                                        int qa, int nq, int end, int imin, int lmax) {
-    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, imin, lmax, pg.page_size, (int)pg.n_pages,
+                                        int qa, int nq, int end, int imin, int lmax, uint32_t recip) {
+    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, imin, lmax, pg.page_size, (int)pg.n_pages, recip,
             pg.table + (int64_t)b * pg.max_pages, pg.kv_sc};
 }
 
@@ -72,7 +75,8 @@ struct __align__(16) Tile {
     int steps;      // steps of 32 keys
     int interior;   // every key is stored and seen by all of them
     int end, sink;  // first position behind the stored tokens; positions below sink stay visible
-    int pad[2];
+    int own;        // 0 = tokens of the shared prefix
+    int n_pages;    // the producer's own
 };
 
 // A tile lies in shared memory, moves and is freed in four parts, in one of two orders of its 8-key x 128-byte
@@ -97,25 +101,25 @@ struct Item {
     int qi[NQ], qlow[NQ];   // each query's token, and the first that its window holds
 };
 
-template <int NQ, int ST>
+template <int NQ, int ST, int W>
 struct Smem {
-    static constexpr int R = kH * NQ;
+    static constexpr int RQ = kH * NQ, R = kH * W;       // rows: of the queries, and of the accumulators
     alignas(1024) uint8_t K[ST][kTileBytes];
-    alignas(1024) uint8_t Qs[kBlocks][2 * R][128];       // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
-    alignas(1024) uint8_t P[3 * NQ][kTileKeys][16];      // [term][query]: 16 rows of each key, no swizzle
+    alignas(1024) uint8_t Qs[kBlocks][2 * RQ][128];      // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
+    alignas(1024) uint8_t P[3 * W][kTileKeys][16];       // [term][query] or [warpgroup][term]: 16 rows of each key, no swizzle
     alignas(16) float sc[ST][kTileKeys];                 // the keys' token scales
     int upos[ST][kTileKeys / kGroup];                    // position of each unit's first key; behind all without a page
     Tile tile[ST];
     alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
     alignas(16) float fac[R];
-    alignas(16) float rowf[2][R];   // by item
+    alignas(16) float rowf[2][RQ];   // by item
     float lsum[4][R];
     Seg seg[NQ + 1];   // the producer's own
     Item<NQ> item[2];
     int dead;
     uint32_t tmem;
-    uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], s_free[2], p_full, pv_done, wind_down[2];
+    uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], s_free[2], p_full[2], pv_done[2], wind_down[2];
     uint64_t item_full[2], item_empty[2], q_full[2];
 };
 
@@ -218,6 +222,21 @@ __device__ __forceinline__ void split_e5m2(uint32_t p, uint32_t& hi, uint32_t& m
     lo = *reinterpret_cast<uint32_t*>(&r) + 0x00800080u;   // the low bytes are not used
 }
 
+// A load that stays where it is written, ahead of the waits of the tile before.
+__device__ __forceinline__ int ldg_now(const int32_t* p) {
+    int v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// A copy of 16 bytes, and an arrival on a barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ int stored_end(const csa2_pages& pg, int b) {
     const int64_t cap = (int64_t)pg.max_pages * pg.page_size;
     int64_t n = pg.n_tokens[b];
@@ -236,22 +255,31 @@ struct KernelArgs {
 };
 
 // NQ queries, ST tiles in flight, the order of a tile's atoms, whether the three terms of P have accumulator columns
-// of their own (one product for all three, 3R columns, where TMEM has room), CTAs on an SM.
-template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas>
-__global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
+// of their own (one product for all three, 3 RQ columns, where TMEM has room), CTAs on an SM.  kPair: one query whose
+// tiles two warpgroups take in turn, each with its own references, P and accumulators: two splits that share the
+// tiles in flight.
+template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas, bool kPair = false>
+__global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     pages_attn_kernel(const __grid_constant__ CUtensorMap map_own, const __grid_constant__ CUtensorMap map_prefix,
                       const __grid_constant__ KernelArgs args) {
-    using Sm = Smem<NQ, ST>;
-    constexpr int R = Sm::R;
+    static_assert(!kPair || (NQ == 1 && kConcat), "a pair takes one query");
+    constexpr int W = kPair ? 2 : NQ;                  // softmax warpgroups
+    using Sm = Smem<NQ, ST, W>;
+    constexpr int RQ = Sm::RQ, R = Sm::R;
     using L = Layout<kByKeys>;
-    constexpr int kOCols = (kConcat ? 3 : 1) * R;      // accumulator columns of one channel block
+    constexpr int kOCols = (kConcat ? 3 : 1) * RQ;     // accumulator columns of one channel block
+    constexpr int kOSet = kPair ? 4 * kOCols : 0;      // from one warpgroup's accumulators to the next's
     constexpr uint32_t kTmemCols = 512 / kCtas;
-    constexpr uint32_t kS0 = 4 * kOCols;               // S^T buffers behind the accumulators
-    static_assert(kS0 + 2 * 2 * R <= kTmemCols, "TMEM budget");
+    constexpr uint32_t kS0 = kOSet + 4 * kOCols;       // S^T buffers behind the accumulators
+    static_assert(kS0 + 2 * 2 * RQ <= kTmemCols, "TMEM budget");
+    // Barrier and parity of tile n's P and of its products: a pair's warpgroups have one each.
+    auto pbar = [](int n) { return kPair ? n & 1 : 0; };
+    auto ppar = [](int n) { return (uint32_t)((kPair ? n >> 1 : n) & 1); };
+    constexpr int kTurn = kPair ? 2 : 1;               // tiles from one of a warpgroup to its next
     extern __shared__ uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const PagesAttnParams& p = args.p;
-    constexpr int kProducer = 4 * NQ, kIssuer = kProducer + 1;   // behind the softmax warpgroups
+    constexpr int kProducer = 4 * W, kIssuer = kProducer + 1;   // behind the softmax warpgroups
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ul = args.unit_log2, unit = 1 << ul, upt = kTileKeys >> ul;   // keys of a unit, units of a tile
 
@@ -259,19 +287,19 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
     if (tid == 32 * kProducer) {
         for (int s = 0; s < ST; ++s)
             for (int c = 0; c < kBlocks; ++c) {
-            mbar_init(&sm.full[s][c], kByKeys && c == 0 ? 2 : 1);   // with the first part come the scales
+            mbar_init(&sm.full[s][c], c == 0 ? 33 : 1);   // with the first part come the scales, by every lane
             mbar_init(&sm.empty[s][c], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], 4 * NQ);
+            mbar_init(&sm.p_full[i], kWg * NQ);
+            mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.wind_down[i], 1);
             mbar_init(&sm.item_full[i], 1);
-            mbar_init(&sm.item_empty[i], 4 * NQ + 2);
-            mbar_init(&sm.q_full[i], 4 * NQ);
+            mbar_init(&sm.item_empty[i], 4 * W + 2);
+            mbar_init(&sm.q_full[i], 4 * W);
         }
-        mbar_init(&sm.p_full, kWg * NQ);
-        mbar_init(&sm.pv_done, 1);
         fence_mbar_init();
         sm.dead = 0;
     }
@@ -317,57 +345,77 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         while (s + 1 < nseg && tile >= sm.seg[s + 1].tile0) ++s;
         return s;
     };
-    // Producer: the copies of tile t, the CTA's n-th, part by part (one lane per unit), and the keys' scales: by a copy
-    // per unit where units are large, else by the lanes' own loads (a copy costs about 50 cycles however small).
-    auto load_tile = [&](int t, int n) -> bool {
-        const int st = n % ST;
-        const Seg& sg = sm.seg[seg_of(t)];
-        const int v = (t - sg.tile0) * upt + lane;
-        int row = -1;
-        if (lane < upt && v < sg.units) {
-            const int slot = sg.unit(v) * unit, pg = slot / sg.page_size, page = __ldg(sg.table + pg);
-            if (page >= 0 && page < sg.n_pages) row = page * sg.page_size + (slot - pg * sg.page_size);
+    // Producer.  A tile is prepared in steps, each a tile ahead of the next, so that no load's latency falls on the
+    // copies: the page of the lane's unit (one lane per unit), the unit's row, the copies.
+    struct Ahead {
+        int page, at;          // the unit's page (not waited for before rows_of), and its first slot in there
+        int row, first;        // its row in the pool (-1: none), its first key's position
+        uint32_t live;         // units that have a row
+        bool inside;           // every query sees all of its keys
+        Tile info;
+        const float* scales;   // of keys 4 lane .. 4 lane + 3, or null
+    };
+    Seg sg;          // the list of the next tile to be read
+    int sg_at = -1;
+    auto page_of = [&](int t) -> Ahead {
+        const int s = seg_of(t);
+        if (s != sg_at) {
+            sg = sm.seg[s];
+            sg_at = s;
         }
-        const int row4 = __shfl_sync(0xFFFFFFFFu, row, (4 * lane) >> ul);   // the unit of keys 4 lane .. 4 lane + 3
-        float4 sc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (kByKeys && row4 >= 0) sc = __ldg(reinterpret_cast<const float4*>(sg.scales + row4 + ((4 * lane) & (unit - 1))));
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, row >= 0);
-        const int first = row >= 0 ? sg.pos0 + sg.unit(v) * unit : 0, last = first + unit - 1;
-        const bool inside = row >= 0 && last < sg.end && last <= sg.imin && (first >= sg.lmax || (sg.own && last < p.n_sink));
-        const int keys = min(kTileKeys, (sg.units - (t - sg.tile0) * upt) * unit);
-        const Tile info = {sg.qa, sg.nq, (keys + 31) / 32, __popc(__ballot_sync(0xFFFFFFFFu, inside)) == upt, sg.end,
-                           sg.own ? p.n_sink : 0};
-        const CUtensorMap* map = sg.own ? &map_own : &map_prefix;
-        auto put_scales = [&] {
-            *reinterpret_cast<float4*>(&sm.sc[st][4 * lane]) = sc;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.full[st][0]);
-        };
+        Ahead a;
+        const int v0 = (t - sg.tile0) * upt, v = v0 + lane, u = sg.unit(min(v, sg.units - 1)), d = sg.page_size >> ul;
+        // u / d, by the quotient's lower bound u floor((2^32 - 1) / d) / 2^32, which is at most 1 too small
+        int i = (int)__umulhi((uint32_t)u, sg.recip), r = u - i * d;
+        if (r >= d) ++i, r -= d;
+        a.page = ldg_now(sg.table + i);   // a load in every lane, so that nothing here depends on it
+        a.at = r << ul;
+        const bool have = lane < upt && v < sg.units;
+        a.first = have ? sg.pos0 + (u << ul) : 0x7FFFFF00;
+        const int last = a.first + unit - 1;
+        a.inside = have && last < sg.end && last <= sg.imin && (a.first >= sg.lmax || (sg.own && last < p.n_sink));
+        const int keys = min(kTileKeys, (sg.units - v0) << ul);
+        a.info = {sg.qa, sg.nq, (keys + 31) / 32, 0, sg.end, sg.own ? p.n_sink : 0, sg.own, sg.n_pages};
+        a.row = sg.page_size;
+        a.scales = sg.scales;
+        return a;
+    };
+    auto rows_of = [&](Ahead& a) {
+        a.row = a.first != 0x7FFFFF00 && a.page >= 0 && a.page < a.info.n_pages ? a.page * a.row + a.at : -1;
+        if (a.row < 0) a.first = 0x7FFFFF00;
+        const int row4 = __shfl_sync(0xFFFFFFFFu, a.row, (4 * lane) >> ul);
+        a.scales = row4 >= 0 ? a.scales + row4 + ((4 * lane) & (unit - 1)) : nullptr;
+        a.live = __ballot_sync(0xFFFFFFFFu, a.row >= 0);
+        a.info.interior = __popc(__ballot_sync(0xFFFFFFFFu, a.inside && a.row >= 0)) == upt;
+    };
+    // The copies of the CTA's n-th tile, part by part, the keys' scales with the first.
+    auto load_tile = [&](const Ahead& a, int n) -> bool {
+        const int st = n % ST;
+        const CUtensorMap* map = a.info.own ? &map_own : &map_prefix;
 #pragma unroll
         for (int c = 0; c < kBlocks; ++c) {
             bool ok = true;
             if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
             if (c == 0) {
-                if (lane < upt) sm.upos[st][lane] = row >= 0 ? first : 0x7FFFFF00;
-                if (lane == 0) sm.tile[st] = info;
+                if (lane < upt) sm.upos[st][lane] = a.first;
+                if (lane == 0) sm.tile[st] = a.info;
+                if (a.scales) cp_async16(&sm.sc[st][4 * lane], a.scales);
+                cp_async_arrive(&sm.full[st][0]);
             }
             const int upp = 32 >> ul;   // by keys: units of a part
-            const uint32_t bytes = kByKeys ? __popc(live & (((1u << upp) - 1u) << (c * upp))) * unit * kD
-                                           : __popc(live) * unit * (c == 0 ? 128 + 4 : 128);
+            const uint32_t bytes =
+                kByKeys ? __popc(a.live & (((1u << upp) - 1u) << (c * upp))) * unit * kD : __popc(a.live) * unit * 128;
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], bytes);
             __syncwarp();
-            if (row >= 0 && !args.test_starve) {
-                if (!kByKeys) {
-                    tma_unit(sm.K[st] + c * L::block + lane * unit * 128, map, row, c, &sm.full[st][c]);
-                    if (c == 0) bulk_load(&sm.sc[st][lane * unit], sg.scales + row, unit * 4, &sm.full[st][0]);
-                } else if (lane >> (5 - ul) == c)
-                    tma_groups(sm.K[st] + lane * unit * kD, map, row / kGroup, &sm.full[st][c]);
+            if (a.row >= 0 && !args.test_starve) {
+                if (!kByKeys)
+                    tma_unit(sm.K[st] + c * L::block + lane * unit * 128, map, a.row, c, &sm.full[st][c]);
+                else if (lane >> (5 - ul) == c)
+                    tma_groups(sm.K[st] + lane * unit * kD, map, a.row / kGroup, &sm.full[st][c]);
             }
-            if (kByKeys && c == 0 && n >= ST) put_scales();
         }
-        if (kByKeys && n < ST) put_scales();   // the first tiles: the copies go out before the scales are back
         return true;
     };
 
@@ -376,6 +424,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         // chain of loads (positions, page table, rows) passes under the item before.
         auto units_of = [&](int n) { return ((n - 1) >> ul) + 1; };   // n >= 1 keys; n + unit - 1 might not fit
         auto tiles_of = [&](int u) { return ((u - 1) >> (7 - ul)) + 1; };
+        const uint32_t recip_own = 0xFFFFFFFFu / (uint32_t)(p.own.page_size >> ul);
+        const uint32_t recip_prefix = shared_prefix ? 0xFFFFFFFFu / (uint32_t)(p.prefix.page_size >> ul) : 0;
         int tile_no = 0;
         bool ok = true;
         for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
@@ -428,7 +478,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
                 if (e > 0) {
                     const int u = units_of(e);
-                    if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
+                    if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0, recip_prefix);
                     n = 1;
                     tiles = tiles_of(u);
                 }
@@ -452,7 +502,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     n += ot > 0;
                     tiles += ot;
                 }
-                if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow);
+                if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow, recip_own);
             }
             nseg = n;
             const int each = tiles / args.splits, extra = tiles - each * args.splits;   // the first splits take one tile more
@@ -472,7 +522,20 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                                  : "memory");
                 }
             }
-            for (int t = 0; ok && t < nt; ++t, ++tile_no) ok = load_tile(t0 + t, tile_no);
+            if (nt > 0) {
+                sg_at = -1;
+                Ahead a = page_of(t0), next = page_of(t0 + min(1, nt - 1));
+                rows_of(a);
+                for (int t = 0;;) {
+                    ok = load_tile(a, tile_no);
+                    if (!ok) break;
+                    ++tile_no;
+                    if (++t == nt) break;
+                    a = next;
+                    if (t + 1 < nt) next = page_of(t0 + t + 1);
+                    rows_of(a);
+                }
+            }
         }
         if (!ok) {   // wind down: the copies in flight land before the CTA ends
             for (int n = max(0, tile_no - ST); n <= tile_no; ++n)
@@ -501,7 +564,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 if (!ok) break;
                 const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
                 const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
-                const uint32_t d = td + kS0 + (n & 1) * 2 * R + 32 * qa, id = idesc_qk(32 * qn);
+                const uint32_t d = td + kS0 + (n & 1) * 2 * RQ + 32 * qa, id = idesc_qk(32 * qn);
 #pragma unroll
                 for (int c = 0; c < kBlocks; ++c) {
                     if (!kByKeys && c > 0) {   // after a wait that ran out the products read what is there; S is not announced
@@ -511,7 +574,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     tc_fence_after();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * R * 128) + s * 32) / 16, id, c + s > 0);
+                        mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * RQ * 128) + s * 32) / 16, id, c + s > 0);
                 }
                 if (!kByKeys) ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -537,14 +600,14 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             const int last = n + __shfl_sync(0xFFFFFFFFu, sm.item[k & 1].tiles, 0);
             for (; n < last && ok; ++n) {
                 const int st = n % ST;
-                ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full, (uint32_t)(n & 1)));
+                ok = __all_sync(0xFFFFFFFFu, wait(&sm.p_full[pbar(n)], ppar(n)));
                 if (!ok) break;
                 const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
                 const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
                 const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128);
                 tc_fence_after();
-                const uint64_t b = pd + qa * (2048 / 16);
-                const uint32_t d = td + kH * qa;
+                const uint64_t b = pd + (qa + 3 * pbar(n)) * (2048 / 16);
+                const uint32_t d = td + kH * qa + pbar(n) * kOSet;
                 // Part i of the tile; its memory is free for a coming tile when its products are done.
                 auto parts = [&](auto product) {
 #pragma unroll
@@ -558,16 +621,16 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     }
                 };
                 if (kConcat && qn == NQ) {   // the three terms as one product
-                    parts([&](int c, uint64_t as, uint64_t bs) { mma_f8(lead, d + c * kOCols, as, bs, idesc_pv(3 * R), 1); });
+                    parts([&](int c, uint64_t as, uint64_t bs) { mma_f8(lead, d + c * kOCols, as, bs, idesc_pv(3 * RQ), 1); });
                 } else {
                     const uint32_t id = idesc_pv(kH * qn);
                     parts([&](int c, uint64_t as, uint64_t bs) {
 #pragma unroll
                         for (int x = 0; x < 3; ++x)
-                            mma_f8(lead, d + c * kOCols + (kConcat ? x * R : 0), as, bs + x * NQ * (2048 / 16), id, 1);
+                            mma_f8(lead, d + c * kOCols + (kConcat ? x * RQ : 0), as, bs + x * NQ * (2048 / 16), id, 1);
                     });
                 }
-                commit(lead, &sm.pv_done);
+                commit(lead, &sm.pv_done[pbar(n)]);
             }
             if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
         }
@@ -577,52 +640,59 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
         }
         __syncwarp();
     } else {
-        // ---- softmax: warpgroup = query, thread = key ----
-        const int wg = warp >> 2, key = tid & (kWg - 1), quarter = warp & 3;
+        // ---- softmax: warpgroup = query (or every other tile of one), thread = key ----
+        const int wg = warp >> 2, query = kPair ? 0 : wg, key = tid & (kWg - 1), quarter = warp & 3;
         const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
-        // this query's accumulator columns: 16 of each channel block (and of each term)
-        auto ocol = [&](int b, int x) -> uint32_t { return tq + b * kOCols + x * R + kH * wg; };
+        // this warpgroup's accumulator columns: 16 of each channel block (and of each term)
+        auto ocol = [&](int b, int x) -> uint32_t { return tq + wg * kOSet + b * kOCols + x * RQ + kH * query; };
         constexpr int kTerms = kConcat ? 3 : 1;
         auto row4 = [&](const float (&a)[R], int j) { return *reinterpret_cast<const float4*>(&a[kH * wg + 4 * j]); };
+        const bool split = kPair || args.splits > 1;   // partial sums go to the workspace
         const int ku = key >> ul, ko = key & (unit - 1);
         int n = 0;
         // Item by item: its queries are converted as soon as the item before has seen its last S, so that the first S
         // of the next is made while the output of the last is written.
         int f0 = 0, nq = 0, nt = 0, prev_f0 = 0, prev_nq = 0;
         int64_t part = 0;
+        int last = -1;   // a pair: this warpgroup's last tile in the item
         for (int k_item = 0, it = blockIdx.x;; ++k_item, it += gridDim.x) {
             const bool have = it < args.items;
-            float(&rowf)[R] = sm.rowf[k_item & 1];
+            float(&rowf)[RQ] = sm.rowf[k_item & 1];
+            auto rowf4 = [&](int j) { return *reinterpret_cast<const float4*>(&rowf[kH * query + 4 * j]); };
             prev_f0 = f0;
             prev_nq = nq;
             if (have) {
-                // Q: four rows (heads) of this query in each warp, 16 channels per lane -> E4M3 hi and lo, each row scaled
+                // Q: four rows (heads; of a pair two) in each warp, 16 channels per lane -> E4M3 hi and lo, each row scaled
                 // so that its largest is in [2^7, 2^8)
                 queries_of(it / args.splits, f0, nq);
-                uint4 v[4][2];
+                constexpr int kRows = 4 * NQ / W;
+                auto head = [&](int k) { return kPair ? warp + 8 * k : quarter + 4 * k; };
+                uint4 v[kRows][2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kRows; ++k) {
                     v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-                    if (wg < nq) {
-                        const int64_t row = (int64_t)(f0 + wg) * kH + quarter + 4 * k;
+                    if (query < nq) {
+                        const int64_t row = (int64_t)(f0 + query) * kH + head(k);
                         const uint4* src = reinterpret_cast<const uint4*>(p.q + row * kD) + 2 * lane;
                         v[k][0] = __ldg(src);
                         v[k][1] = __ldg(src + 1);
                     }
                 }
-                const bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
+                bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
+                // the other warpgroup's last S of the item before still reads Q
+                if (kPair && n > 0) told = wait(&sm.s_full[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1)) && told;
                 if (wg_any(wg, !told)) break;   // a wait ran out: no item to work on
-                uint32_t top[4];   // bits of the row's largest |bf16|; from 0x7F80 on the row holds an infinity or NaN
+                uint32_t top[kRows];   // bits of the row's largest |bf16|; from 0x7F80 on the row holds an infinity or NaN
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kRows; ++k) {
                     const uint32_t t = __vmaxu2(bf16x8_topbits(v[k][0]), bf16x8_topbits(v[k][1]));
                     top[k] = __reduce_max_sync(0xFFFFFFFFu, max(t & 0xFFFFu, t >> 16));
                     // such a row enters the products as zeros and gets its NaN by rowf: S is NaN only where K is
                     if (top[k] >= 0x7F80u) v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int h = quarter + 4 * k, r = kH * wg + h;
+                for (int k = 0; k < kRows; ++k) {
+                    const int h = head(k), r = kH * query + h;
                     const int e = max((int)(top[k] >> 7) - 127 - 7, -120);
                     const float mul = __uint_as_float((uint32_t)(127 - e) << 23);
                     uint32_t hi[4], lo[4];
@@ -642,7 +712,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b2) : "f"(x[3] - y[3]), "f"(x[2] - y[2]));
                         lo[j] = (uint32_t)a | ((uint32_t)b2 << 16);
                     }
-                    const int rh = 32 * wg + h, rl = rh + 16, at = ((lane & 7) ^ (rh & 7)) << 4;   // rl & 7 is the same
+                    const int rh = 32 * query + h, rl = rh + 16, at = ((lane & 7) ^ (rh & 7)) << 4;   // rl & 7 is the same
                     *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rh][at]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(&sm.Qs[lane >> 3][rl][at]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     const float scale = __uint_as_float((uint32_t)(127 + e) << 23) * (p.sm_scale * 1.4426950408889634f);
@@ -658,17 +728,18 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 if (key < kH) {
                     const int r = kH * wg + key;
                     const float sum = (sm.lsum[0][r] + sm.lsum[1][r]) + (sm.lsum[2][r] + sm.lsum[3][r]), ref = sm.mref[r];
-                    if (args.splits > 1) {
+                    if (split) {
                         float* ml = args.part_ml + (part * R + r) * 2;
                         *reinterpret_cast<float2*>(ml) = make_float2(ref, sum);
-                    } else if (p.lse && wg < prev_nq) {
-                        p.lse[(int64_t)(prev_f0 + wg) * kH + key] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+                    } else if (p.lse && query < prev_nq) {
+                        p.lse[(int64_t)(prev_f0 + query) * kH + key] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
                     }
                     sm.mref[r] = -INFINITY;   // for the next item
-                    sm.fac[r] = (args.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum) * (1.0f / kPScale);
+                    sm.fac[r] = (split ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum) * (1.0f / kPScale);
                 }
                 wg_bar(wg);
-                if (nt > 0) wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+                const int done = kPair ? last : nt > 0 ? n - 1 : -1;
+                if (done >= 0) wait(&sm.pv_done[pbar(done)], ppar(done));
                 tc_fence_after();
                 float fac[kH];
 #pragma unroll
@@ -678,7 +749,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 }
                 float* po = args.part_o + (part * R + kH * wg) * kD;
                 // bf16 out: lanes 2 i and 2 i + 1 trade rows, so that each stores two channels of eight rows
-                uint16_t* out = p.out + ((int64_t)(prev_f0 + wg) * kH + 8 * (lane & 1)) * kD + (key & ~1);
+                uint16_t* out = p.out + ((int64_t)(prev_f0 + query) * kH + 8 * (lane & 1)) * kD + (key & ~1);
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     uint32_t o[kTerms][16];
@@ -693,10 +764,10 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                         for (int x = 1; x < kTerms; ++x) y[h] += __uint_as_float(o[x][h]);
                         y[h] *= fac[h];
                     }
-                    if (args.splits > 1) {
+                    if (split) {
 #pragma unroll
                         for (int h = 0; h < kH; ++h) po[h * kD + 128 * b + key] = y[h];
-                    } else if (wg < prev_nq) {
+                    } else if (query < prev_nq) {
 #pragma unroll
                         for (int h = 0; h < 8; ++h) {
                             const uint32_t own = pack_bf16(y[h], y[h + 8]), other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
@@ -711,7 +782,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
             if (!have) break;
 
             const Item<NQ>& item = sm.item[k_item & 1];
-            const int qi = item.qi[wg], qlow = item.qlow[wg];
+            const int qi = item.qi[query], qlow = item.qlow[query];
             nt = item.tiles;
             part = item.part;
             __syncwarp();
@@ -724,17 +795,22 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     for (int x = 0; x < kTerms; ++x) tmem_st_x16(ocol(b, x), zero);
                 tmem_st_wait();
             }
-            wg_bar(wg);   // rowf of the whole query
+            if (kPair)   // rowf of the whole query
+                wait(&sm.q_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
+            else
+                wg_bar(wg);
+            last = -1;
             float l[kH];
 #pragma unroll
             for (int h = 0; h < kH; ++h) l[h] = 0.0f;
 
             // After a wait that ran out the loop goes on with what is there: every thread passes every named barrier.
             for (int i = 0; i < nt; ++i, ++n) {
+                if (kPair && (n & 1) != wg) continue;
                 const int st = n % ST;
                 bool ok = wait(&sm.full[st][0], (uint32_t)((n / ST) & 1));   // the scales and what the producer says of the tile
                 const Tile tile = sm.tile[st];
-                const bool active = wg >= tile.qa && wg < tile.qa + tile.nq;   // this tile's products cover this query
+                const bool active = kPair || (wg >= tile.qa && wg < tile.qa + tile.nq);   // this tile's products cover this query
                 bool seen = active;
                 if (!tile.interior) {
                     const int pos = sm.upos[st][ku] + ko;
@@ -748,18 +824,19 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                     const float lsc = fmaxf(__log2f(ts), kMinLogScale);
                     float x[kH];   // logits in log2 units less the rows' references
                     auto sums = [&](uint32_t (&u)[32]) {   // hi in u[0 .. 15], lo in u[16 .. 31]
-                        tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * R + 32 * wg, u);
+                        tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * RQ + 32 * query, u);
                         tmem_ld_wait();
                         dirty = !seen && isnan(__uint_as_float(u[0]));
                     };
-                    bool move = i == 0;
-                    if (i > 0) {
+                    const bool first = i < kTurn;
+                    bool move = first;
+                    if (!first) {
                         uint32_t u[32];
                         sums(u);
                         float top = -INFINITY;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float4 f4 = row4(rowf, j), m4 = row4(sm.mref, j);
+                            const float4 f4 = rowf4(j), m4 = row4(sm.mref, j);
                             const float f[4] = {f4.x, f4.y, f4.z, f4.w}, m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
@@ -779,7 +856,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                             sums(u);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float4 f4 = row4(rowf, j);
+                                const float4 f4 = rowf4(j);
                                 const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) {
@@ -805,8 +882,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                             sm.mref[r] = fmaxf(m, old);
                         }
                         wg_bar(wg);
-                        if (i > 0) {
-                            wait(&sm.pv_done, (uint32_t)((n - 1) & 1));
+                        if (!first) {
+                            wait(&sm.pv_done[pbar(n)], ppar(n - kTurn));
                             tc_fence_after();
 #pragma unroll 1
                             for (int b = 0; b < kBlocks; ++b)
@@ -821,7 +898,7 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                             }
                             tmem_st_wait();
                         }
-                        if (i > 0) {
+                        if (!first) {
 #pragma unroll
                             for (int h = 0; h < kH; ++h) l[h] *= sm.fac[kH * wg + h];
                         }
@@ -855,17 +932,17 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                         w[1][j] = __byte_perm(m0, m1, 0x7531);
                         w[2][j] = __byte_perm(l0, l1, 0x7531);
                     }
-                    if (n > 0) ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;   // P is free when the last tile's products are done
+                    if (n >= kTurn) ok = wait(&sm.pv_done[pbar(n)], ppar(n - kTurn)) && ok;   // P is free when the last tile's products are done
 #pragma unroll
                     for (int y = 0; y < 3; ++y)
-                        *reinterpret_cast<uint4*>(&sm.P[y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+                        *reinterpret_cast<uint4*>(&sm.P[kPair ? 3 * wg + y : y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
                 } else if (n > 0) {
                     // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
-                    ok = wait(&sm.pv_done, (uint32_t)((n - 1) & 1)) && ok;
+                    ok = wait(&sm.pv_done[0], ppar(n - 1)) && ok;
                 }
                 if (!active && lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
                 if (dirty && ok) {   // S of this tile is done: only P K still reads the row
-                    for (int b = wg - tile.qa; b < kBlocks; b += tile.nq)
+                    for (int b = query - tile.qa; b < kBlocks; b += tile.nq)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             *reinterpret_cast<uint4*>(&sm.K[st][(key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7)]) =
@@ -873,7 +950,8 @@ __global__ void __launch_bounds__(kWg * NQ + kAux, kCtas)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                if (ok) mbar_arrive(&sm.p_full);
+                if (ok) mbar_arrive(&sm.p_full[pbar(n)]);
+                if (kPair) last = n;
             }
             // ---- row sums over the 128 threads ----
             {
@@ -974,6 +1052,8 @@ __global__ void __launch_bounds__(128 * kGroups) pages_merge_kernel(const __grid
 
 struct Plan {
     int nq, blocks, splits;
+    bool pair;  // one query, two warpgroups: each leaves a part of its own
+    int parts;  // partial results of a block
     bool two;   // two CTAs on an SM, one tile in flight each; else one CTA with all its tiles
     size_t o_bytes, bytes;
 };
@@ -988,18 +1068,19 @@ Plan plan(bool prefix, int B, int Q, int64_t keys) {
     pl.nq = together >= 3 ? 4 : (int)together;
     pl.two = pl.nq <= 2;
     pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
-    const int64_t ctas = pl.two ? 2 * kSplitSMs : kSplitSMs;
-    int64_t s = ctas / pl.blocks;
     const int64_t most = tiles < 4 ? 1 : tiles;   // up to three tiles cost a CTA less than the join does
-    if (s > most) s = most;
-    if (s < 1) s = 1;
-    pl.splits = (int)s;
-    // One query: with few tiles and CTAs, all of them in flight at once (one token, 132 keys: 8.4 us against 9.6);
-    // with many, two CTAs whose phases alternate (61 queries of 4,096 keys: 46.5 us against 53.5).
+    auto splits = [&](int64_t ctas) { return std::max<int64_t>(1, std::min(ctas / pl.blocks, most)); };
+    int64_t s = splits(pl.two ? 2 * kSplitSMs : kSplitSMs);
     if (pl.nq == 1 && tiles <= 3 * s && pl.blocks * s <= kSplitSMs) pl.two = false;
+    if (pl.nq == 1 && pl.two) {
+        pl.two = false, pl.pair = true;
+        s = splits(kSplitSMs);
+    }
+    pl.splits = (int)s;
+    pl.parts = pl.splits * (pl.pair ? 2 : 1);
     pl.bytes = 256;
-    if (s > 1) {
-        const size_t rows = (size_t)pl.blocks * s * kH * pl.nq;
+    if (pl.parts > 1) {
+        const size_t rows = (size_t)pl.blocks * pl.parts * kH * pl.nq;
         pl.o_bytes = rows * kD * 4;
         pl.bytes += pl.o_bytes + rows * 8;
     }
@@ -1045,14 +1126,15 @@ cudaError_t pool_map(const csa2_pages& pg, int unit, bool by_keys, CUtensorMap* 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas>
+template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas, bool kPair = false>
 cudaError_t launch(const KernelArgs& a, const CUtensorMap& own, const CUtensorMap& prefix, cudaStream_t st) {
     static DeviceOnce attr;
-    const auto kernel = pages_attn_kernel<NQ, ST, kByKeys, kConcat, kCtas>;
-    const int smem = (int)sizeof(Smem<NQ, ST>) + 1024, most = device_sm_count() * kCtas;
+    const auto kernel = pages_attn_kernel<NQ, ST, kByKeys, kConcat, kCtas, kPair>;
+    constexpr int W = kPair ? 2 : NQ;
+    const int smem = (int)sizeof(Smem<NQ, ST, W>) + 1024, most = device_sm_count() * kCtas;
     cudaError_t e = attr.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
     if (e != cudaSuccess) return e;
-    return launch_ex(kernel, dim3(most > 0 && a.items > most ? most : a.items), dim3(kWg * NQ + kAux), smem, st, 0, own, prefix, a);
+    return launch_ex(kernel, dim3(most > 0 && a.items > most ? most : a.items), dim3(kWg * W + kAux), smem, st, 0, own, prefix, a);
 }
 
 }  // namespace
@@ -1085,14 +1167,16 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
         e = pool_map(p.prefix, unit, by_keys, &mp);
         if (e != cudaSuccess) return e;
     }
-    e = pl.nq == 1 && pl.two ? launch<1, 1, true, true, 2>(a, mo, mp, st)
+    e = pl.pair              ? launch<1, 3, true, true, 1, true>(a, mo, mp, st)
+        : pl.nq == 1 && pl.two ? launch<1, 1, true, true, 2>(a, mo, mp, st)
         : pl.nq == 1         ? launch<1, 3, true, true, 1>(a, mo, mp, st)
         : pl.nq == 2 ? launch<2, 1, true, false, 2>(a, mo, mp, st)
         : by_keys    ? launch<4, 2, true, false, 1>(a, mo, mp, st)
                      : launch<4, 2, false, false, 1>(a, mo, mp, st);
-    if (e != cudaSuccess || pl.splits == 1) return e;
+    if (e != cudaSuccess || pl.parts == 1) return e;
+    a.splits = pl.parts;
     const dim3 rows((unsigned)(p.B * p.Q * kH));
-    return pl.splits < kMergeMany ? launch_ex(pages_merge_kernel<1>, rows, dim3(128), 0, st, 0, a, pl.nq)
+    return pl.parts < kMergeMany ? launch_ex(pages_merge_kernel<1>, rows, dim3(128), 0, st, 0, a, pl.nq)
                                   : launch_ex(pages_merge_kernel<4>, rows, dim3(512), 0, st, 0, a, pl.nq);
 }
 
