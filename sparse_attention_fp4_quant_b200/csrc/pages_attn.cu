@@ -56,7 +56,6 @@ struct Seg {
     int pos0, end;  // position of slot 0, and of the first slot behind the stored tokens
     int imin, lmax;  // every query of the list sees the stored tokens in [lmax, imin]
     int page_size, n_pages;
-    uint32_t recip;         // floor((2^32 - 1) / units of a page)
     const int32_t* table;   // the sequence's row
     const float* scales;
 
@@ -64,8 +63,8 @@ struct Seg {
 };
 
 __device__ __forceinline__ Seg make_seg(const csa2_pages& pg, int own, int b, int tile0, int units, int sink, int delta,
-                                        int qa, int nq, int end, int imin, int lmax, uint32_t recip) {
-    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, imin, lmax, pg.page_size, (int)pg.n_pages, recip,
+                                        int qa, int nq, int end, int imin, int lmax) {
+    return {tile0, units, sink, delta, own, qa, nq, pg.pos0, end, imin, lmax, pg.page_size, (int)pg.n_pages,
             pg.table + (int64_t)b * pg.max_pages, pg.kv_sc};
 }
 
@@ -244,12 +243,26 @@ __device__ __forceinline__ int stored_end(const csa2_pages& pg, int b) {
     return (int)(pg.pos0 + n);
 }
 
+// Division of n < 2^32 by d >= 1: n floor((2^32 - 1) / d) / 2^32 is at most 1 below the quotient.  A division
+// instruction sequence takes some 150 cycles, and an item's first copies wait for four of them.
+struct Div {
+    uint32_t d, m;
+
+    __device__ __forceinline__ int operator()(int n) const {
+        const uint32_t q = __umulhi((uint32_t)n, m);
+        return (int)(q + ((uint32_t)n - q * d >= d ? 1u : 0u));
+    }
+};
+Div div_by(int64_t d) { return {(uint32_t)d, 0xFFFFFFFFu / (uint32_t)d}; }
+
 struct KernelArgs {
     PagesAttnParams p;
     int items;        // blocks x splits; CTA i takes items i, i + gridDim.x, ...
     int unit_log2;    // keys of a TMA box: 8 .. 128, divides every page
     int splits;
     int test_starve;  // test hook (csa2_test_starve_copies): the producer issues no copies
+    Div by_splits, by_q, by_per;          // by splits, Q, a sequence's blocks
+    Div by_page_own, by_page_prefix;      // by a page's units
     float* part_o;    // [block][split][R][512]
     float* part_ml;   // [block][split][R][2]
 };
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
             f0 = block * NQ;
             nq = min(NQ, p.B * p.Q - f0);
         } else {
-            const int per = (p.Q + NQ - 1) / NQ, b = block / per, q0 = (block - b * per) * NQ;
+            const int b = args.by_per(block), q0 = (block - b * (int)args.by_per.d) * NQ;
             f0 = b * p.Q + q0;
             nq = min(NQ, p.Q - q0);
         }
@@ -364,10 +377,9 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
             sg_at = s;
         }
         Ahead a;
-        const int v0 = (t - sg.tile0) * upt, v = v0 + lane, u = sg.unit(min(v, sg.units - 1)), d = sg.page_size >> ul;
-        // u / d, by the quotient's lower bound u floor((2^32 - 1) / d) / 2^32, which is at most 1 too small
-        int i = (int)__umulhi((uint32_t)u, sg.recip), r = u - i * d;
-        if (r >= d) ++i, r -= d;
+        const int v0 = (t - sg.tile0) * upt, v = v0 + lane, u = sg.unit(min(v, sg.units - 1));
+        const int d = sg.page_size >> ul;   // units of a page
+        const int i = (sg.own ? args.by_page_own : args.by_page_prefix)(u), r = u - i * d;
         a.page = ldg_now(sg.table + i);   // a load in every lane, so that nothing here depends on it
         a.at = r << ul;
         const bool have = lane < upt && v < sg.units;
@@ -424,19 +436,17 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         // chain of loads (positions, page table, rows) passes under the item before.
         auto units_of = [&](int n) { return ((n - 1) >> ul) + 1; };   // n >= 1 keys; n + unit - 1 might not fit
         auto tiles_of = [&](int u) { return ((u - 1) >> (7 - ul)) + 1; };
-        const uint32_t recip_own = 0xFFFFFFFFu / (uint32_t)(p.own.page_size >> ul);
-        const uint32_t recip_prefix = shared_prefix ? 0xFFFFFFFFu / (uint32_t)(p.prefix.page_size >> ul) : 0;
         int tile_no = 0;
         bool ok = true;
         for (int k = 0, it = blockIdx.x; ok && it < args.items; ++k, it += gridDim.x) {
             if (k >= 2) ok = __all_sync(0xFFFFFFFFu, wait(&sm.item_empty[k & 1], (uint32_t)((k / 2 - 1) & 1)));
             if (!ok) break;
-            const int block = it / args.splits, split = it - block * args.splits;
+            const int block = args.by_splits(it), split = it - block * args.splits;
             int f0, nq;
             queries_of(block, f0, nq);
             // lanes 0 .. NQ-1: a query each
             int i = -1, low = 0, end = 0, pend = 0;
-            const int b = (f0 + min(lane, nq - 1)) / p.Q;
+            const int b = args.by_q(f0 + min(lane, nq - 1));
             if (lane < nq) i = p.q_pos[f0 + lane];
             if (lane < NQ) end = stored_end(p.own, b);
             if (shared_prefix && lane == 0) pend = stored_end(p.prefix, 0);
@@ -478,7 +488,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                 const int e = (imax < pend ? imax + 1 : pend) - p.prefix.pos0;
                 if (e > 0) {
                     const int u = units_of(e);
-                    if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0, recip_prefix);
+                    if (lane == 0) sm.seg[0] = make_seg(p.prefix, 0, 0, 0, u, 0, 0, 0, nq, pend, imin, 0);
                     n = 1;
                     tiles = tiles_of(u);
                 }
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                     n += ot > 0;
                     tiles += ot;
                 }
-                if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow, recip_own);
+                if (u > 0) sm.seg[at] = make_seg(p.own, 1, b, tile0, u, us, uw - us, lane, count, end, rmin, rlow);
             }
             nseg = n;
             const int each = tiles / args.splits, extra = tiles - each * args.splits;   // the first splits take one tile more
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                 mbar_arrive(&sm.item_full[k & 1]);
                 if (it + gridDim.x < args.items) {   // the next item's queries on their way to L2
                     int g0, gn;
-                    queries_of((it + gridDim.x) / args.splits, g0, gn);
+                    queries_of(args.by_splits(it + gridDim.x), g0, gn);
                     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + (int64_t)g0 * kH * kD),
                                  "r"(gn * kH * kD * 2)
                                  : "memory");
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
             if (have) {
                 // Q: four rows (heads; of a pair two) in each warp, 16 channels per lane -> E4M3 hi and lo, each row scaled
                 // so that its largest is in [2^7, 2^8)
-                queries_of(it / args.splits, f0, nq);
+                queries_of(args.by_splits(it), f0, nq);
                 constexpr int kRows = 4 * NQ / W;
                 auto head = [&](int k) { return kPair ? warp + 8 * k : quarter + 4 * k; };
                 uint4 v[kRows][2];
@@ -1159,6 +1169,11 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
     int unit = by_keys ? (far ? 32 : 16) : divides(128) ? 128 : 64;
     while (!divides(unit)) unit /= 2;
     while ((1 << a.unit_log2) < unit) ++a.unit_log2;
+    a.by_splits = div_by(pl.splits);
+    a.by_q = div_by(p.Q);
+    a.by_per = div_by((p.Q + pl.nq - 1) / pl.nq);
+    a.by_page_own = div_by(p.own.page_size / unit);
+    a.by_page_prefix = div_by(prefix ? p.prefix.page_size / unit : 1);
     CUtensorMap mo, mp;
     cudaError_t e = pool_map(p.own, unit, by_keys, &mo);
     if (e != cudaSuccess) return e;
