@@ -942,7 +942,8 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                         w[1][j] = __byte_perm(m0, m1, 0x7531);
                         w[2][j] = __byte_perm(l0, l1, 0x7531);
                     }
-                    if (n >= kTurn) ok = wait(&sm.pv_done[pbar(n)], ppar(n - kTurn)) && ok;   // P is free when the last tile's products are done
+                    // P is free when the products of the warpgroup's last tile are done
+                    if (n >= kTurn) ok = wait(&sm.pv_done[pbar(n)], ppar(n - kTurn)) && ok;
 #pragma unroll
                     for (int y = 0; y < 3; ++y)
                         *reinterpret_cast<uint4*>(&sm.P[kPair ? 3 * wg + y : y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
@@ -955,8 +956,10 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                     for (int b = query - tile.qa; b < kBlocks; b += tile.nq)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4*>(&sm.K[st][(key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7)]) =
-                                make_uint4(0, 0, 0, 0);
+                        {
+                            const uint32_t at = (key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7);
+                            *reinterpret_cast<uint4*>(&sm.K[st][at]) = make_uint4(0, 0, 0, 0);
+                        }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -987,20 +990,23 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the splits of a block: one CTA per row, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).  The weights
-// come first, a thread per split, so that the loads of the partial rows do not wait on one another.  With many splits
-// four groups of 128 threads take every fourth one (12 queries in 49 splits: 36 us in all against 44 with one group);
-// with few one group does (61 queries in 4 splits: 45.5 against 47.6).
-constexpr int kMergeMany = 12;   // splits from which on four groups join them
-template <int kGroups>
-__global__ void __launch_bounds__(128 * kGroups) pages_merge_kernel(const __grid_constant__ KernelArgs args, int NQ) {
+// Joins the splits of a block, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).  The weights come first, a thread
+// per split, so that the loads of the partial rows do not wait on one another.  Few splits: a CTA of 128 threads per
+// row.  Twelve and more: four groups of 128 threads that take every fourth split (12 queries in 49 splits 36 us in all
+// against 44 with one group; 61 queries in 4 splits 47.6 against 45.5).  64 and more, which leave few rows: four CTAs per
+// row, 128 channels each, whose 16 warps take every sixteenth split (one query, 131,072 keys, 296 parts: 26.0 us in all
+// against 38.3 with four groups; four queries of 74 parts 55.0 against 57.9; four of 49 parts 17.7 against 17.0).
+constexpr int kMergeMany = 12, kMergeSlice = 64;
+template <int kGroups, int kLanes>
+__global__ void __launch_bounds__(kGroups * kLanes) pages_merge_kernel(const __grid_constant__ KernelArgs args, int NQ) {
     pdl_enter();
-    __shared__ float w[kMaxSplits], red[4 * kGroups], red2[4 * kGroups];
-    __shared__ float4 part[kGroups][128];
+    constexpr int kWarps = kGroups * kLanes / 32;
+    __shared__ float w[kMaxSplits], red[kWarps], red2[kWarps];
+    __shared__ float4 part[kGroups][kLanes];
     static_assert(kMaxSplits <= 512 && kMergeMany <= 128, "a thread per split");
     const PagesAttnParams& p = args.p;
     const int S = args.splits, R = kH * NQ, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int group = tid >> 7, col = tid & 127;
+    const int group = tid / kLanes, at = tid % kLanes, col = blockIdx.y * kLanes + at;
     const int f = blockIdx.x / kH, h = blockIdx.x % kH;
     int blk, c;
     if (p.prefix.B) {
@@ -1019,7 +1025,7 @@ __global__ void __launch_bounds__(128 * kGroups) pages_merge_kernel(const __grid
     __syncthreads();
     float M = red[0];
 #pragma unroll
-    for (int i = 1; i < 4 * kGroups; ++i) M = fmaxf(M, red[i]);
+    for (int i = 1; i < kWarps; ++i) M = fmaxf(M, red[i]);
     const float Mu = M == -INFINITY ? 0.0f : M;
     const float e = exp2f(v.x - Mu);
     if (tid < S) w[tid] = e;
@@ -1041,30 +1047,30 @@ __global__ void __launch_bounds__(128 * kGroups) pages_merge_kernel(const __grid
     }
     L = red2[0];
 #pragma unroll
-    for (int i = 1; i < 4 * kGroups; ++i) L += red2[i];
+    for (int i = 1; i < kWarps; ++i) L += red2[i];
     if (kGroups > 1) {
-        if (group > 0) part[group][col] = o;
+        if (group > 0) part[group][at] = o;
         __syncthreads();
         if (group > 0) return;
 #pragma unroll
         for (int g = 1; g < kGroups; ++g) {
-            const float4 y = part[g][col];
+            const float4 y = part[g][at];
             o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
         }
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     *reinterpret_cast<uint2*>(p.out + (int64_t)blockIdx.x * kD + 4 * col) =
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (p.lse && tid == 0) p.lse[blockIdx.x] = L == 0.0f ? -INFINITY : (Mu + log2f(L)) * 0.6931471805599453f;
+    if (p.lse && tid == 0 && blockIdx.y == 0) p.lse[blockIdx.x] = L == 0.0f ? -INFINITY : (Mu + log2f(L)) * 0.6931471805599453f;
 }
 
 // ---- host ----------------------------------------------------------------------------------
 
 struct Plan {
     int nq, blocks, splits;
-    bool pair;  // one query, two warpgroups: each leaves a part of its own
+    bool two;   // two CTAs on an SM, one tile in flight each
+    bool pair;  // one query by two warpgroups, each of which leaves a part of its own
     int parts;  // partial results of a block
-    bool two;   // two CTAs on an SM, one tile in flight each; else one CTA with all its tiles
     size_t o_bytes, bytes;
 };
 
@@ -1081,10 +1087,16 @@ Plan plan(bool prefix, int B, int Q, int64_t keys) {
     const int64_t most = tiles < 4 ? 1 : tiles;   // up to three tiles cost a CTA less than the join does
     auto splits = [&](int64_t ctas) { return std::max<int64_t>(1, std::min(ctas / pl.blocks, most)); };
     int64_t s = splits(pl.two ? 2 * kSplitSMs : kSplitSMs);
-    if (pl.nq == 1 && tiles <= 3 * s && pl.blocks * s <= kSplitSMs) pl.two = false;
-    if (pl.nq == 1 && pl.two) {
-        pl.two = false, pl.pair = true;
-        s = splits(kSplitSMs);
+    // One query.  With few tiles and CTAs, all of them in flight in one CTA (8 queries of 1,000 keys 9.9 us against 11.8 by
+    // a pair, one of 132 keys 8.4 against 9.6 by two CTAs).  Else a pair, whose two warpgroups share three tiles in flight,
+    // where a CTA has one item or long ones (148 queries of 640 keys 19.6 us against 24.6 by two CTAs, 300 of 4,096 150
+    // against 195); two CTAs of one tile each where items are many and short, so that one works while the other changes
+    // its item (250 of 500 keys 23.3 us against 31.2 by a pair, 600 of 1,024 92.7 against 96.8).
+    if (pl.nq == 1) {
+        const bool few = tiles <= 3 * s && pl.blocks * s <= kSplitSMs;
+        pl.pair = !few && (pl.blocks <= kSplitSMs || tiles >= 16);
+        pl.two = !few && !pl.pair;
+        if (pl.pair) s = splits(kSplitSMs);
     }
     pl.splits = (int)s;
     pl.parts = pl.splits * (pl.pair ? 2 : 1);
@@ -1190,9 +1202,10 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
                      : launch<4, 2, false, false, 1>(a, mo, mp, st);
     if (e != cudaSuccess || pl.parts == 1) return e;
     a.splits = pl.parts;
-    const dim3 rows((unsigned)(p.B * p.Q * kH));
-    return pl.parts < kMergeMany ? launch_ex(pages_merge_kernel<1>, rows, dim3(128), 0, st, 0, a, pl.nq)
-                                  : launch_ex(pages_merge_kernel<4>, rows, dim3(512), 0, st, 0, a, pl.nq);
+    const unsigned rows = (unsigned)(p.B * p.Q * kH);
+    return pl.parts < kMergeMany   ? launch_ex(pages_merge_kernel<1, 128>, dim3(rows), dim3(128), 0, st, 0, a, pl.nq)
+           : pl.parts < kMergeSlice ? launch_ex(pages_merge_kernel<4, 128>, dim3(rows), dim3(512), 0, st, 0, a, pl.nq)
+                                    : launch_ex(pages_merge_kernel<16, 32>, dim3(rows, 4), dim3(512), 0, st, 0, a, pl.nq);
 }
 
 }  // namespace csa2

@@ -374,6 +374,75 @@ def test_keys_that_a_nan_query_does_not_see(csa, ps, value):
     assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
 
 
+# ---- single queries with long lists: two warpgroups take a query's tiles in turn --------------
+
+def long_lists(seed, B, n, page, **kw):
+    """Sequences around the tiles' borders, a third of the others up to n tokens, the rest short."""
+    rng = np.random.default_rng(seed)
+    lens = [int(v) for v in np.where(np.arange(B) % 3 == 0, rng.integers(0, n, B), rng.integers(0, 300, B))]
+    lens[:11] = [n, 0, 1, 127, 128, 129, 255, 256, 257, 384, 385]
+    return lens, Cache(seed, lens, page, **kw)
+
+
+@pytest.mark.parametrize("B,n,window,sink,page", [
+    (60, 2300, 1 << 30, 0, 16), (160, 2200, 2100, 5, 64), (100, 700, 1 << 30, 0, 8), (148, 640, 600, 70, 24), (320, 2049, 2048, 1, 32)])
+def test_long_lists(csa, B, n, window, sink, page):
+    lens, cache = long_lists(B, B, n, page)
+    q, q_pos = queries(B, B, 1), tail_positions(lens, 1)
+    out, lse = run_window(csa, cache, q, q_pos, window, sink)
+    check(out, lse, reference(q, q_pos, [(cache, True)], window, sink))
+
+
+def test_long_lists_masked_nan_and_bad_queries(csa):
+    lens, cache = long_lists(3, 60, 2300, 16)
+    q, q_pos = queries(6, 60, 1), tail_positions(lens, 1)
+    clean = run_window(csa, cache, q, q_pos, 2200, 9)
+    cache.poison_dead({cache.row(b, j) for b in range(60) for i in q_pos[b] for j in visible(cache, b, int(i), 2200, 9)})
+    bad = q.clone()
+    bad[0, 0, 0, 3], bad[20, 0, 15, 400] = float("nan"), float("inf")
+    out, lse = run_window(csa, cache, bad, q_pos, 2200, 9)
+    keep = torch.ones((60, 1, H), dtype=torch.bool)
+    keep[0, 0, 0] = keep[20, 0, 15] = False
+    keep = keep.cuda()
+    assert out[~keep].isnan().all() and lse[~keep].isnan().all()
+    assert torch.equal(out[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
+def test_long_lists_extreme_keys_and_queries(csa):
+    lens = [2000] * 2 + [3] * 58
+    cache = Cache(22, lens, 64)
+    order = [cache.row(0, j) for j in range(2000)]
+    for j in (0, 5, 1999):
+        cache.kv[order[j]], cache.kv_sc[order[j]] = 0, 0.0
+    for j in range(100, 200):
+        cache.kv_sc[order[j]] *= 1e-20
+    for j in list(range(300, 310)) + [700, 1500, 1900]:
+        cache.kv_sc[order[j]] *= 30.0
+    q, q_pos = queries(5, 60, 1), tail_positions(lens, 1)
+    q[0, :, 3] = 0
+    q[0, :, 4] *= 2.0 ** 100
+    q[0, :, 5] *= 2.0 ** -100
+    q[0, 0, 6] = torch.from_numpy(E4M3[cache.kv[order[1000]]]).to(torch.bfloat16) * 0.05   # looks straight at token 1000
+    q[1, 0, 6] = torch.from_numpy(E4M3[cache.kv[cache.row(1, 130)]]).to(torch.bfloat16) * 0.05
+    q[0, :, 7, 100] = 300.0
+    out, lse = run_window(csa, cache, q, q_pos, 1 << 30, 0)
+    check(out, lse, reference(q, q_pos, [(cache, True)], None, 0))
+
+
+@pytest.mark.parametrize("n", [9000, 60000])
+def test_many_splits(csa, n):
+    """Splits by the hundred: a row's join is shared by several CTAs."""
+    lens = [n, n // 3]
+    cache = Cache(n, lens, 64)
+    q, q_pos = queries(7, 2, 1), tail_positions(lens, 1)
+    out, lse = run_window(csa, cache, q, q_pos, 1 << 30, 0)
+    check(out, lse, reference(q, q_pos, [(cache, True)], None, 0))
+    prefix, own = Cache(n + 1, [n], 64), Cache(n + 2, [1, 70, 0, 5], 64, pos0=n)
+    q, q_pos = queries(8, 4, 1), np.array([[n], [n + 69], [n - 1], [n + 4]], np.int32)
+    out, lse = run_prefix(csa, prefix, own, q, q_pos)
+    check(out, lse, reference(q, q_pos, [(prefix, False), (own, True)]))
+
+
 # ---- as they are used --------------------------------------------------------------------------
 
 def test_decode_run(csa):
@@ -576,3 +645,19 @@ def test_timeout_is_reported(csa):
         csa.csa2_flag_status()
     check(*run_window(csa, cache, q, q_pos, 128, 4), reference(q, q_pos, [(cache, True)], 128, 4))
     check(*run_prefix(csa, prefix, own, q, pq_pos), reference(q, pq_pos, [(prefix, False), (own, True)]))
+
+
+def test_timeout_of_long_lists(csa):
+    """The same where two warpgroups share a query."""
+    lens, cache = long_lists(5, 60, 2300, 16)
+    q, q_pos = queries(6, 60, 1), tail_positions(lens, 1)
+    csa.csa2_flag_status()
+    csa.lib().csa2_test_starve_copies(1)
+    try:
+        csa.csa2_window_attn(q.cuda(), cache.gpu(), torch.from_numpy(q_pos).cuda(), window=2200)
+        with pytest.raises(csa.CSA2Error, match="TIMEOUT"):
+            csa.csa2_flag_status(clear=True)
+    finally:
+        csa.lib().csa2_test_starve_copies(0)
+    csa.csa2_flag_status()
+    check(*run_window(csa, cache, q, q_pos, 2200, 4), reference(q, q_pos, [(cache, True)], 2200, 4))
