@@ -78,19 +78,13 @@ struct __align__(16) Tile {
     int n_pages;    // the producer's own
 };
 
-// A tile lies in shared memory, moves and is freed in four parts, in one of two orders of its 8-key x 128-byte
-// swizzle atoms:
-//   by channels  [4 channel blocks][16 key groups]: a part is a channel block.  S takes a part as it lands, and O
-//                frees one while the next is in work, so the wait for the next tile is short; a copy moves one
-//                channel block of a unit, which pays for units of 64 keys and more.
-//   by keys      [16 key groups][4 channel blocks]: a part is 32 keys.  One copy moves all channels of a unit: with
-//                pages of 16 tokens a tile takes 1,060 cycles to fetch, against 2,340 by channels.
-template <bool kByKeys>
-struct Layout {
-    static constexpr uint32_t group = kByKeys ? 4096 : 1024;      // from one 8-key group to the next
-    static constexpr uint32_t block = kByKeys ? 1024 : 16384;     // from one channel block to the next
-    static constexpr uint32_t step = 4 * group;                   // 32 keys
-};
+// A tile lies in shared memory as 8-key x 128-byte swizzle atoms, [16 key groups][4 channel blocks], and moves and is
+// freed in four parts of 32 keys.  One copy moves all channels of a unit: with pages of 16 tokens a tile takes 1,060
+// cycles to fetch.  (The other order, [4 channel blocks][16 key groups], lets S begin with a quarter of the tile, but
+// moves a unit by four copies: 2,340 cycles, and with pages of 64 tokens no faster: 32 queries behind 131,072 tokens 174
+// us either way.)
+constexpr int kParts = 4;
+constexpr uint32_t kGroupStep = 4096, kBlockStep = 1024, kPartStep = 4 * kGroupStep;   // bytes from one to the next
 
 // A CTA's item (queries and a split of their keys): what the producer tells the other roles.
 template <int NQ>
@@ -118,7 +112,7 @@ struct Smem {
     Item<NQ> item[2];
     int dead;
     uint32_t tmem;
-    uint64_t full[ST][kBlocks], empty[ST][kBlocks], s_full[2], s_free[2], p_full[2], pv_done[2], wind_down[2];
+    uint64_t full[ST][kParts], empty[ST][kParts], s_full[2], s_free[2], p_full[2], pv_done[2], wind_down[2];
     uint64_t item_full[2], item_empty[2], q_full[2];
 };
 
@@ -154,16 +148,8 @@ __device__ __forceinline__ uint32_t idesc_pv(int N) {
 }
 constexpr uint32_t kSw128 = 2;
 
-// Channel block c of one unit's rows, or all channels of one unit's 8-key groups.
-__device__ __forceinline__ void tma_unit(void* dst, const CUtensorMap* map, int row, int c, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(0), "r"(row), "r"(c), "r"(smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_groups(void* dst, const CUtensorMap* map, int group, uint64_t* bar) {
+// All channels of one unit's 8-key groups.
+__device__ __forceinline__ void tma_unit(void* dst, const CUtensorMap* map, int group, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], "
         "[%4];" ::"r"(smem_u32(dst)),
@@ -258,7 +244,7 @@ Div div_by(int64_t d) { return {(uint32_t)d, 0xFFFFFFFFu / (uint32_t)d}; }
 struct KernelArgs {
     PagesAttnParams p;
     int items;        // blocks x splits; CTA i takes items i, i + gridDim.x, ...
-    int unit_log2;    // keys of a TMA box: 8 .. 128, divides every page
+    int unit_log2;    // keys of a TMA box: 8, 16 or 32, divides every page
     int splits;
     int test_starve;  // test hook (csa2_test_starve_copies): the producer issues no copies
     Div by_splits, by_q, by_per;          // by splits, Q, a sequence's blocks
@@ -267,11 +253,10 @@ struct KernelArgs {
     float* part_ml;   // [block][split][R][2]
 };
 
-// NQ queries, ST tiles in flight, the order of a tile's atoms, whether the three terms of P have accumulator columns
-// of their own (one product for all three, 3 RQ columns, where TMEM has room), CTAs on an SM.  kPair: one query whose
-// tiles two warpgroups take in turn, each with its own references, P and accumulators: two splits that share the
-// tiles in flight.
-template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas, bool kPair = false>
+// NQ queries, ST tiles in flight, whether the three terms of P have accumulator columns of their own (one product for
+// all three, 3 RQ columns, where TMEM has room), CTAs on an SM.  kPair: one query whose tiles two warpgroups take in turn,
+// each with its own references, P and accumulators: two splits that share the tiles in flight.
+template <int NQ, int ST, bool kConcat, int kCtas, bool kPair = false>
 __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     pages_attn_kernel(const __grid_constant__ CUtensorMap map_own, const __grid_constant__ CUtensorMap map_prefix,
                       const __grid_constant__ KernelArgs args) {
@@ -279,7 +264,6 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     constexpr int W = kPair ? 2 : NQ;                  // softmax warpgroups
     using Sm = Smem<NQ, ST, W>;
     constexpr int RQ = Sm::RQ, R = Sm::R;
-    using L = Layout<kByKeys>;
     constexpr int kOCols = (kConcat ? 3 : 1) * RQ;     // accumulator columns of one channel block
     constexpr int kOSet = kPair ? 4 * kOCols : 0;      // from one warpgroup's accumulators to the next's
     constexpr uint32_t kTmemCols = 512 / kCtas;
@@ -299,10 +283,10 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     if (warp == kIssuer) tmem_alloc(&sm.tmem, kTmemCols);
     if (tid == 32 * kProducer) {
         for (int s = 0; s < ST; ++s)
-            for (int c = 0; c < kBlocks; ++c) {
-            mbar_init(&sm.full[s][c], c == 0 ? 33 : 1);   // with the first part come the scales, by every lane
-            mbar_init(&sm.empty[s][c], 1);
-        }
+            for (int c = 0; c < kParts; ++c) {
+                mbar_init(&sm.full[s][c], c == 0 ? 33 : 1);   // with the first part come the scales, by every lane
+                mbar_init(&sm.empty[s][c], 1);
+            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], 4 * NQ);
@@ -405,7 +389,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         const int st = n % ST;
         const CUtensorMap* map = a.info.own ? &map_own : &map_prefix;
 #pragma unroll
-        for (int c = 0; c < kBlocks; ++c) {
+        for (int c = 0; c < kParts; ++c) {
             bool ok = true;
             if (n >= ST) ok = wait(&sm.empty[st][c], (uint32_t)((n / ST - 1) & 1));
             if (!__all_sync(0xFFFFFFFFu, ok)) return false;
@@ -415,18 +399,13 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                 if (a.scales) cp_async16(&sm.sc[st][4 * lane], a.scales);
                 cp_async_arrive(&sm.full[st][0]);
             }
-            const int upp = 32 >> ul;   // by keys: units of a part
-            const uint32_t bytes =
-                kByKeys ? __popc(a.live & (((1u << upp) - 1u) << (c * upp))) * unit * kD : __popc(a.live) * unit * 128;
+            const int upp = 32 >> ul;   // units of a part
+            const uint32_t bytes = __popc(a.live & (((1u << upp) - 1u) << (c * upp))) * unit * kD;
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm.full[st][c], bytes);
             __syncwarp();
-            if (a.row >= 0 && !args.test_starve) {
-                if (!kByKeys)
-                    tma_unit(sm.K[st] + c * L::block + lane * unit * 128, map, a.row, c, &sm.full[st][c]);
-                else if (lane >> (5 - ul) == c)
-                    tma_groups(sm.K[st] + lane * unit * kD, map, a.row / kGroup, &sm.full[st][c]);
-            }
+            if (a.row >= 0 && lane >> (5 - ul) == c && !args.test_starve)
+                tma_unit(sm.K[st] + lane * unit * kD, map, a.row / kGroup, &sm.full[st][c]);
         }
         return true;
     };
@@ -549,7 +528,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         }
         if (!ok) {   // wind down: the copies in flight land before the CTA ends
             for (int n = max(0, tile_no - ST); n <= tile_no; ++n)
-                for (int c = 0; c < kBlocks; ++c) mbar_wait(&sm.full[n % ST][c], (uint32_t)((n / ST) & 1), kTimeoutNs / 16);
+                for (int c = 0; c < kParts; ++c) mbar_wait(&sm.full[n % ST][c], (uint32_t)((n / ST) & 1), kTimeoutNs / 16);
         }
     } else if (warp == kIssuer) {
         // ---- S issuer.  S and O have a warp each: one thread issues a product in about 50 cycles, more than most of
@@ -567,27 +546,20 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
             for (; n < last && ok; ++n) {
                 const int st = n % ST;
                 if (n >= 2) ok = wait(&sm.s_free[n & 1], (uint32_t)((n / 2 - 1) & 1));
-                const int first_parts = kByKeys ? kBlocks : 1;
 #pragma unroll
-                for (int c = 0; c < first_parts; ++c) ok = ok && wait(&sm.full[st][c], (uint32_t)((n / ST) & 1));
+                for (int c = 0; c < kParts; ++c) ok = ok && wait(&sm.full[st][c], (uint32_t)((n / ST) & 1));
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
-                const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128), b = qd + qa * (4096 / 16);
+                const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, kGroupStep, kSw128), b = qd + qa * (4096 / 16);
                 const uint32_t d = td + kS0 + (n & 1) * 2 * RQ + 32 * qa, id = idesc_qk(32 * qn);
+                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kBlocks; ++c) {
-                    if (!kByKeys && c > 0) {   // after a wait that ran out the products read what is there; S is not announced
-                        ok = wait(&sm.full[st][c], (uint32_t)((n / ST) & 1)) && ok;
-                        __syncwarp();
-                    }
-                    tc_fence_after();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_f8(lead, d, a + (c * L::block + s * 32) / 16, b + (c * (2 * RQ * 128) + s * 32) / 16, id, c + s > 0);
+                        mma_f8(lead, d, a + (c * kBlockStep + s * 32) / 16, b + (c * (2 * RQ * 128) + s * 32) / 16, id, c + s > 0);
                 }
-                if (!kByKeys) ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
                 commit(lead, &sm.s_full[n & 1]);
             }
             if (lane == 0) mbar_arrive(&sm.item_empty[k & 1]);
@@ -614,20 +586,18 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                 if (!ok) break;
                 const int qa = __shfl_sync(0xFFFFFFFFu, sm.tile[st].qa, 0), qn = __shfl_sync(0xFFFFFFFFu, sm.tile[st].nq, 0);
                 const int steps = __shfl_sync(0xFFFFFFFFu, sm.tile[st].steps, 0);
-                const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, L::group, kSw128);
+                const uint64_t a = smem_desc(k0 + st * kTileBytes, 16, kGroupStep, kSw128);
                 tc_fence_after();
                 const uint64_t b = pd + (qa + 3 * pbar(n)) * (2048 / 16);
                 const uint32_t d = td + kH * qa + pbar(n) * kOSet;
                 // Part i of the tile; its memory is free for a coming tile when its products are done.
                 auto parts = [&](auto product) {
 #pragma unroll
-                    for (int i = 0; i < kBlocks; ++i) {
+                    for (int s = 0; s < kParts; ++s) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int c = kByKeys ? j : i, s = kByKeys ? i : j;
-                            if (s < steps) product(c, a + (c * L::block + s * L::step) / 16, b + s * (512 / 16));
-                        }
-                        commit(lead, &sm.empty[st][i]);
+                        for (int c = 0; c < kBlocks; ++c)
+                            if (s < steps) product(c, a + (c * kBlockStep + s * kPartStep) / 16, b + s * (512 / 16));
+                        commit(lead, &sm.empty[st][s]);
                     }
                 };
                 if (kConcat && qn == NQ) {   // the three terms as one product
@@ -957,7 +927,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                         {
-                            const uint32_t at = (key >> 3) * L::group + b * L::block + (key & 7) * 128 + 16 * ((j + key) & 7);
+                            const uint32_t at = (key >> 3) * kGroupStep + b * kBlockStep + (key & 7) * 128 + 16 * ((j + key) & 7);
                             *reinterpret_cast<uint4*>(&sm.K[st][at]) = make_uint4(0, 0, 0, 0);
                         }
                 }
@@ -1126,32 +1096,23 @@ EncodeFn encoder() {
     return fn;
 }
 
-// The pool as a tensor whose boxes land in the tile's order: by channels [4 channel blocks][rows][128 B], a box being
-// one block of a unit's rows; by keys [groups of 8 rows][4 channel blocks][8 rows][128 B], a box being a unit's groups.
-cudaError_t pool_map(const csa2_pages& pg, int unit, bool by_keys, CUtensorMap* map) {
+// The pool as a tensor [groups of 8 rows][4 channel blocks][8 rows][128 B], a box being a unit's groups: they land in the
+// tile's order.
+cudaError_t pool_map(const csa2_pages& pg, int unit, CUtensorMap* map) {
     const EncodeFn fn = encoder();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t rows = (cuuint64_t)(pg.n_pages * pg.page_size);
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    CUresult r;
-    if (by_keys) {
-        const cuuint64_t dims[4] = {128, kGroup, kBlocks, rows / kGroup}, strides[3] = {kD, 128, (cuuint64_t)kGroup * kD};
-        const cuuint32_t box[4] = {128, kGroup, kBlocks, (cuuint32_t)(unit / kGroup)};
-        r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    } else {
-        const cuuint64_t dims[3] = {128, rows, kBlocks}, strides[2] = {kD, 128};
-        const cuuint32_t box[3] = {128, (cuuint32_t)unit, 1};
-        r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    }
+    const cuuint64_t dims[4] = {128, kGroup, kBlocks, rows / kGroup}, strides[3] = {kD, 128, (cuuint64_t)kGroup * kD};
+    const cuuint32_t es[4] = {1, 1, 1, 1}, box[4] = {128, kGroup, kBlocks, (cuuint32_t)(unit / kGroup)};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int NQ, int ST, bool kByKeys, bool kConcat, int kCtas, bool kPair = false>
+template <int NQ, int ST, bool kConcat, int kCtas, bool kPair = false>
 cudaError_t launch(const KernelArgs& a, const CUtensorMap& own, const CUtensorMap& prefix, cudaStream_t st) {
     static DeviceOnce attr;
-    const auto kernel = pages_attn_kernel<NQ, ST, kByKeys, kConcat, kCtas, kPair>;
+    const auto kernel = pages_attn_kernel<NQ, ST, kConcat, kCtas, kPair>;
     constexpr int W = kPair ? 2 : NQ;
     const int smem = (int)sizeof(Smem<NQ, ST, W>) + 1024, most = device_sm_count() * kCtas;
     cudaError_t e = attr.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
@@ -1173,13 +1134,10 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
     a.test_starve = test_starve_copies();
     a.part_o = (float*)ws;
     a.part_ml = (float*)((char*)ws + pl.o_bytes);
-    // A unit lies in one page.  Large ones cost fewer copies; a window's first unit reaches back over up to unit - 1
-    // keys that no query sees.
-    const bool far = prefix || p.window >= 512;
-    auto divides = [&](int u) { return p.own.page_size % u == 0 && (!prefix || p.prefix.page_size % u == 0); };
-    const bool by_keys = !(pl.nq == 4 && far && divides(64));
-    int unit = by_keys ? (far ? 32 : 16) : divides(128) ? 128 : 64;
-    while (!divides(unit)) unit /= 2;
+    // A unit lies in one page.  Units of 32 keys cost half as many copies as 16 (300 queries of 4,096 keys 148.5 us against
+    // 153.5); a short window takes 16, as its first unit reaches back over up to unit - 1 keys that no query sees.
+    int unit = prefix || p.window >= 512 ? 32 : 16;
+    while (p.own.page_size % unit || (prefix && p.prefix.page_size % unit)) unit /= 2;
     while ((1 << a.unit_log2) < unit) ++a.unit_log2;
     a.by_splits = div_by(pl.splits);
     a.by_q = div_by(p.Q);
@@ -1187,19 +1145,18 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
     a.by_page_own = div_by(p.own.page_size / unit);
     a.by_page_prefix = div_by(prefix ? p.prefix.page_size / unit : 1);
     CUtensorMap mo, mp;
-    cudaError_t e = pool_map(p.own, unit, by_keys, &mo);
+    cudaError_t e = pool_map(p.own, unit, &mo);
     if (e != cudaSuccess) return e;
     mp = mo;
     if (prefix && (p.prefix.kv != p.own.kv || p.prefix.n_pages * p.prefix.page_size != p.own.n_pages * p.own.page_size)) {
-        e = pool_map(p.prefix, unit, by_keys, &mp);
+        e = pool_map(p.prefix, unit, &mp);
         if (e != cudaSuccess) return e;
     }
-    e = pl.pair              ? launch<1, 3, true, true, 1, true>(a, mo, mp, st)
-        : pl.nq == 1 && pl.two ? launch<1, 1, true, true, 2>(a, mo, mp, st)
-        : pl.nq == 1         ? launch<1, 3, true, true, 1>(a, mo, mp, st)
-        : pl.nq == 2 ? launch<2, 1, true, false, 2>(a, mo, mp, st)
-        : by_keys    ? launch<4, 2, true, false, 1>(a, mo, mp, st)
-                     : launch<4, 2, false, false, 1>(a, mo, mp, st);
+    e = pl.nq == 4   ? launch<4, 2, false, 1>(a, mo, mp, st)
+        : pl.nq == 2 ? launch<2, 1, false, 2>(a, mo, mp, st)
+        : pl.pair    ? launch<1, 3, true, 1, true>(a, mo, mp, st)
+        : pl.two     ? launch<1, 1, true, 2>(a, mo, mp, st)
+                     : launch<1, 3, true, 1>(a, mo, mp, st);
     if (e != cudaSuccess || pl.parts == 1) return e;
     a.splits = pl.parts;
     const unsigned rows = (unsigned)(p.B * p.Q * kH);
