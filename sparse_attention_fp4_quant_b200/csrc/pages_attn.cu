@@ -20,6 +20,15 @@
 // rescaled rarely.  l = sum 2^(z - m) stays in fp32 registers.
 // A slot that no query sees may hold NaN bytes, and a weight of 0 times NaN is NaN.  Such a key's
 // S is NaN as well, so its thread finds out for nothing, and zeroes the row before P K.
+//
+// What bounds it (B200, calls in a graph; the join included):
+//   many queries over long lists  the tensor pipe: 64 rows x 128 keys are 16 products of 64 cycles for S and 48 of 48
+//       cycles for O, 3,340 of the 4,700 or so that a tile takes.  32 queries behind 131,072 tokens 173 us, 0.48 of the time
+//       of the products at the measured bf16 rate; 3 x 1,017 queries of a 1,024-token window 153 us, 0.36.
+//   one query, long lists         the stream: 61 queries of 4,096 tokens in pages of 16 38 us, 5.6 TB/s while it runs.
+//   many queries, short windows   a chain of 19,700 cycles an item (queries in, two tiles, output): 4,096 queries of a
+//       128-token window 79 us.
+//   one token                     the same chain after the launch: 8 us for 1 to 32 sequences.
 #include <cuda.h>
 
 #include <algorithm>
@@ -1051,10 +1060,14 @@ Plan plan(bool prefix, int B, int Q, int64_t keys) {
     const int64_t together = prefix ? n : Q;   // queries that share keys
     int64_t tiles = (keys + kTileKeys - 1) / kTileKeys + (prefix ? 1 : 0);
     if (tiles < 1) tiles = 1;
+    // Four queries share a tile's copies and products (4,096 queries of a short window 85 us against 105 with two in each
+    // of two CTAs).
     pl.nq = together >= 3 ? 4 : (int)together;
     pl.two = pl.nq <= 2;
     pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
-    const int64_t most = tiles < 4 ? 1 : tiles;   // up to three tiles cost a CTA less than the join does
+    // Up to three tiles cost a CTA no more than the join does (one query of 384 keys 8.8 us whole, 9.6 split; of 512 12.0
+    // and 9.8; four queries of 384 15.9 and 14.8, of 512 18.2 and 15.1; a caller's workspace not counted).
+    const int64_t most = tiles < 4 ? 1 : tiles;
     auto splits = [&](int64_t ctas) { return std::max<int64_t>(1, std::min(ctas / pl.blocks, most)); };
     int64_t s = splits(pl.two ? 2 * kSplitSMs : kSplitSMs);
     // One query.  With few tiles and CTAs, all of them in flight in one CTA (8 queries of 1,000 keys 9.9 us against 11.8 by
