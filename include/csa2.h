@@ -505,7 +505,8 @@ CSA2_API csa2_status csa2_window_attn(const void* q, const csa2_pages* pages, co
  * own sequence's tokens.  The query at token i of sequence b sees the tokens
  * j <= i of `prefix` and of `pages` row b.
  *   prefix  host pointer, prefix->B == 1
- *   pages   host pointer: the sequences' own tokens, usually with pos0 = the prefix's length
+ *   pages   host pointer: the sequences' own tokens, usually with pos0 = the prefix's length; a
+ *           position that both hold is two tokens, and both are seen
  *   q, q_pos, out, lse, ws, flag: as for csa2_window_attn (CSA2_OP_PREFIX_ATTN)
  */
 CSA2_API csa2_status csa2_prefix_attn(const void* q, const csa2_pages* prefix, const csa2_pages* pages,

@@ -610,6 +610,8 @@ def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None
                      out=None, lse=False, ws=None):
     """Sliding-window attention over a paged cache; tokens at positions below n_sink stay visible.
     q bf16 [B,Q,16,512], q_pos i32 [B,Q] (negative = no query) -> out bf16 [B,Q,16,512] (, lse f32 [B,Q,16])."""
+    if not (-2 ** 31 <= window < 2 ** 31 and -2 ** 31 <= n_sink < 2 ** 31):   # ctypes would cut them off
+        raise ValueError(f"window and n_sink are 32-bit numbers, got {window} and {n_sink}")
     dev = torch.cuda.current_device()
     pg, flag = pages.c(dev), _flag(dev)
     out, lse, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_WINDOW_ATTN, q, q_pos, pages, min(window + n_sink, pages.cap),

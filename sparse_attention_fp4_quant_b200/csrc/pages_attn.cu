@@ -110,7 +110,7 @@ struct Smem {
     alignas(1024) uint8_t Qs[kBlocks][2 * RQ][128];      // [channel block][query][hi 16 | lo 16][128 B], 128-byte swizzle
     alignas(1024) uint8_t P[3 * W][kTileKeys][16];       // [term][query] or [warpgroup][term]: 16 rows of each key, no swizzle
     alignas(16) float sc[ST][kTileKeys];                 // the keys' token scales
-    int upos[ST][kTileKeys / kGroup];                    // position of each unit's first key; behind all without a page
+    int upos[ST][kTileKeys / kGroup];                    // position of each unit's first key; -1 without a page
     Tile tile[ST];
     alignas(16) float wmax[4][R];
     alignas(16) float mref[R];
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     // Producer.  A tile is prepared in steps, each a tile ahead of the next, so that no load's latency falls on the
     // copies: the page of the lane's unit (one lane per unit), the unit's row, the copies.
     struct Ahead {
-        int page, at;          // the unit's page (not waited for before rows_of), and its first slot in there
+        int page, at;          // the unit's page (not waited for before rows_of), and its first slot in there; -1: no unit
         int row, first;        // its row in the pool (-1: none), its first key's position
         uint32_t live;         // units that have a row
         bool inside;           // every query sees all of its keys
@@ -374,9 +374,9 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         const int d = sg.page_size >> ul;   // units of a page
         const int i = (sg.own ? args.by_page_own : args.by_page_prefix)(u), r = u - i * d;
         a.page = ldg_now(sg.table + i);   // a load in every lane, so that nothing here depends on it
-        a.at = r << ul;
         const bool have = lane < upt && v < sg.units;
-        a.first = have ? sg.pos0 + (u << ul) : 0x7FFFFF00;
+        a.at = have ? r << ul : -1;
+        a.first = sg.pos0 + (u << ul);
         const int last = a.first + unit - 1;
         a.inside = have && last < sg.end && last <= sg.imin && (a.first >= sg.lmax || (sg.own && last < p.n_sink));
         const int keys = min(kTileKeys, (sg.units - v0) << ul);
@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         return a;
     };
     auto rows_of = [&](Ahead& a) {
-        a.row = a.first != 0x7FFFFF00 && a.page >= 0 && a.page < a.info.n_pages ? a.page * a.row + a.at : -1;
-        if (a.row < 0) a.first = 0x7FFFFF00;
+        a.row = a.at >= 0 && a.page >= 0 && a.page < a.info.n_pages ? a.page * a.row + a.at : -1;
+        if (a.row < 0) a.first = -1;
         const int row4 = __shfl_sync(0xFFFFFFFFu, a.row, (4 * lane) >> ul);
         a.scales = row4 >= 0 ? a.scales + row4 + ((4 * lane) & (unit - 1)) : nullptr;
         a.live = __ballot_sync(0xFFFFFFFFu, a.row >= 0);
@@ -802,8 +802,8 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                 const bool active = kPair || (wg >= tile.qa && wg < tile.qa + tile.nq);   // this tile's products cover this query
                 bool seen = active;
                 if (!tile.interior) {
-                    const int pos = sm.upos[st][ku] + ko;
-                    seen = active && pos < tile.end && pos <= qi && (pos >= qlow || pos < tile.sink);
+                    const int first_pos = sm.upos[st][ku], pos = first_pos + ko;
+                    seen = active && first_pos >= 0 && pos < tile.end && pos <= qi && (pos >= qlow || pos < tile.sink);
                 }
                 const float ts = seen ? sm.sc[st][key] : 0.0f;
                 bool dirty = false;

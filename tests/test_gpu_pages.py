@@ -296,6 +296,18 @@ def test_window_table_that_starts_later(csa, Q):
         check(out, lse, reference(q, q_pos, [(cache, True)], window, sink))
 
 
+@pytest.mark.parametrize("Q", [1, 4])
+def test_positions_up_to_the_last(csa, Q):
+    """Tables that end just below 2^31: every position is a position, none a mark for "no token"."""
+    for pos0 in (2 ** 31 - 129 - 128, 2 ** 31 - 256 - 16, 2 ** 31 - 129):
+        cache = Cache(19, [128], 16, pos0=pos0)
+        cache.table[0, 5] = -1
+        q, q_pos = queries(10, 1, Q), tail_positions([128], Q) + pos0
+        for window, sink in ((70, 0), (100, pos0 + 3), (1 << 30, 5)):
+            out, lse = run_window(csa, cache, q, q_pos, window, sink)
+            check(out, lse, reference(q, q_pos, [(cache, True)], window, sink))
+
+
 @pytest.mark.parametrize("page_prefix,page_own", [(64, 16), (8, 128), (256, 64), (24, 40)])
 def test_prefix_pages_of_another_size(csa, page_prefix, page_own):
     prefix, mine = Cache(51, [777], page_prefix), Cache(52, [130, 1, 64, 9, 300], page_own, pos0=777)

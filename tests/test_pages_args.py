@@ -97,3 +97,10 @@ def test_binding_refuses(csa):
     with pytest.raises(ValueError):
         csa.Pages.of(*t.values(), pos0=-1)
     csa.Pages.of(*t.values())
+
+
+@pytest.mark.parametrize("window,n_sink", [(2 ** 32 + 5, 0), (2 ** 31, 0), (128, 2 ** 32), (-2 ** 32 + 5, 4)])
+def test_window_beyond_32_bits_is_refused(csa, window, n_sink):
+    """Not cut down to some other window."""
+    with pytest.raises(ValueError, match="32-bit"):
+        csa.csa2_window_attn(None, None, None, window=window, n_sink=n_sink)
