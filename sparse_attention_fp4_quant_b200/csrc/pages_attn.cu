@@ -904,28 +904,33 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
-                    const float tp = ts * kPScale;
-                    uint32_t w[3][4];
+                    if (quarter < tile.steps) {   // else P K stops before this warp's keys
+                        const float tp = ts * kPScale;
+                        uint32_t w[3][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float e[4];
+                        for (int j = 0; j < 4; ++j) {
+                            float e[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            e[i] = ex2(x[4 * j + i]);
-                            l[4 * j + i] += e[i];
+                            for (int i = 0; i < 4; ++i) {
+                                e[i] = ex2(x[4 * j + i]);
+                                l[4 * j + i] += e[i];
+                            }
+                            uint32_t h0, m0, l0, h1, m1, l1;
+                            split_e5m2(pack_f16(e[0] * tp, e[1] * tp), h0, m0, l0);
+                            split_e5m2(pack_f16(e[2] * tp, e[3] * tp), h1, m1, l1);
+                            w[0][j] = __byte_perm(h0, h1, 0x7531);
+                            w[1][j] = __byte_perm(m0, m1, 0x7531);
+                            w[2][j] = __byte_perm(l0, l1, 0x7531);
                         }
-                        uint32_t h0, m0, l0, h1, m1, l1;
-                        split_e5m2(pack_f16(e[0] * tp, e[1] * tp), h0, m0, l0);
-                        split_e5m2(pack_f16(e[2] * tp, e[3] * tp), h1, m1, l1);
-                        w[0][j] = __byte_perm(h0, h1, 0x7531);
-                        w[1][j] = __byte_perm(m0, m1, 0x7531);
-                        w[2][j] = __byte_perm(l0, l1, 0x7531);
-                    }
-                    // P is free when the products of the warpgroup's last tile are done
-                    if (n >= kTurn) ok = wait(&sm.pv_done[pbar(n)], ppar(n - kTurn)) && ok;
+                        // P is free when the products of the warpgroup's last tile are done
+                        if (n >= kTurn) ok = wait(&sm.pv_done[pbar(n)], ppar(n - kTurn)) && ok;
 #pragma unroll
-                    for (int y = 0; y < 3; ++y)
-                        *reinterpret_cast<uint4*>(&sm.P[kPair ? 3 * wg + y : y * NQ + wg][key][0]) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+                        for (int y = 0; y < 3; ++y)
+                            *reinterpret_cast<uint4*>(&sm.P[kPair ? 3 * wg + y : y * NQ + wg][key][0]) =
+                                make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+                    } else if (n >= kTurn) {
+                        ok = wait(&sm.pv_done[pbar(n)], ppar(n - kTurn)) && ok;
+                    }
                 } else if (n > 0) {
                     // a warpgroup that sits a tile out must not arrive for it before the last tile's arrivals are complete
                     ok = wait(&sm.pv_done[0], ppar(n - 1)) && ok;
