@@ -587,7 +587,7 @@ def _pages_attn_args(op, q, q_pos, pages, keys, out, lse, ws, dev):
         op_ = _on(out, torch.bfloat16, n * H * D, "out", dev)
     lp = None
     if lse is True:
-        lse = q.new_empty((B, Q, H), dtype=torch.float32)
+        lse = q.new_empty_strided((B, Q, H), (Q * H, H, 1), dtype=torch.float32)   # 0.3 us less than new_empty
         lp = lse.data_ptr()
     elif lse is False or lse is None:
         lse = None
@@ -603,7 +603,7 @@ def _pages_attn_args(op, q, q_pos, pages, keys, out, lse, ws, dev):
         nbytes = _ws_bytes[key] = lib().csa2_workspace_bytes(op, B, Q, keys, 0, 0)
     if nbytes <= 256:   # nothing is split: the call does not touch it
         return out, lse, Q, qp, pp, op_, lp, _flag(dev), nbytes
-    return out, lse, Q, qp, pp, op_, lp, q.new_empty((nbytes,), dtype=torch.uint8).data_ptr(), nbytes
+    return out, lse, Q, qp, pp, op_, lp, q.new_empty_strided((nbytes,), (1,), dtype=torch.uint8).data_ptr(), nbytes
 
 
 def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None, sm_scale=1.0 / math.sqrt(D),

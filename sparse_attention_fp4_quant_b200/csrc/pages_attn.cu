@@ -27,7 +27,7 @@
 //       of the products at the measured bf16 rate; 3 x 1,017 queries of a 1,024-token window 153 us, 0.36.
 //   one query, long lists         the stream: 61 queries of 4,096 tokens in pages of 16 38 us, 5.6 TB/s while it runs.
 //   many queries, short windows   a chain of 19,700 cycles an item (queries in, two tiles, output): 4,096 queries of a
-//       128-token window 79 us.
+//       128-token window 77 us.
 //   one token                     the same chain after the launch: 8 us for 1 to 32 sequences.
 #include <cuda.h>
 
