@@ -24,8 +24,9 @@
 // What bounds it (B200, calls in a graph; the join included):
 //   many queries over long lists  64 rows x 128 keys are 16 products of 64 cycles for S and 48 of 48 cycles for O, 3,340
 //       of the 5,200 that a tile takes: two tiles fit beside the queries, and a tile's turn (fetch 900 cycles after the
-//       last product of the one before, S 2,200, softmax 2,600, O 3,100, waits) is 10,400 for every second one.  32 queries behind 131,072 tokens 173 us, 0.48 of the time
-//       of the products at the measured bf16 rate; 3 x 1,017 queries of a 1,024-token window 153 us, 0.36.
+//       last product of the one before, S 2,200, softmax 2,600, O 3,100, waits) is 10,400 for every second one.  32
+//       queries behind 131,072 tokens 173 us, 0.48 of the time of the products at the measured bf16 rate; 3 x 1,017 of a
+//       1,024-token window 153 us, 0.36.
 //   one query, long lists         the stream: 61 queries of 4,096 tokens in pages of 16 38 us, 5.6 TB/s while it runs.
 //   many queries, short windows   a chain of 19,700 cycles an item (queries in, two tiles, output): 4,096 queries of a
 //       128-token window 77 us.
