@@ -1067,16 +1067,17 @@ Plan plan(bool prefix, int B, int Q, int64_t keys) {
     const int64_t together = prefix ? n : Q;   // queries that share keys
     int64_t tiles = (keys + kTileKeys - 1) / kTileKeys + (prefix ? 1 : 0);
     if (tiles < 1) tiles = 1;
-    // Four queries share a tile's copies and products (4,096 queries of a short window 85 us against 105 with two in each
-    // of two CTAs).
-    pl.nq = together >= 3 ? 4 : (int)together;
-    pl.two = pl.nq <= 2;
-    pl.blocks = (int)(prefix ? (n + pl.nq - 1) / pl.nq : (int64_t)B * ((Q + pl.nq - 1) / pl.nq));
+    // Four queries share a tile's copies and products where there is much work: 100 x 4 queries of 640 keys 24 us against 42
+    // with a query in each CTA, 4 x 128 of a 128-token window 13.7 against 21.5.  While it fits the GPU about once, single
+    // queries have the shorter chain: 4 queries of a 128-token window 7.8 us against 12.5, 4 behind 4,096 tokens 13.2
+    // against 17.6, 16 behind 4,096 16.8 against 20.4; the two meet at about 1,000 tiles (32 behind 4,096 23.5 and 22.6).
+    pl.nq = together == 1 || (n <= 2 * kSplitSMs && n * tiles <= 1024) ? 1 : 4;
+    pl.blocks = (int)(pl.nq == 1 ? n : prefix ? (n + 3) / 4 : (int64_t)B * ((Q + 3) / 4));
     // Up to three tiles cost a CTA no more than the join does (one query of 384 keys 8.8 us whole, 9.6 split; of 512 12.0
     // and 9.8; four queries of 384 15.9 and 14.8, of 512 18.2 and 15.1; a caller's workspace not counted).
     const int64_t most = tiles < 4 ? 1 : tiles;
     auto splits = [&](int64_t ctas) { return std::max<int64_t>(1, std::min(ctas / pl.blocks, most)); };
-    int64_t s = splits(pl.two ? 2 * kSplitSMs : kSplitSMs);
+    int64_t s = splits(pl.nq == 1 ? 2 * kSplitSMs : kSplitSMs);
     // One query.  With few tiles and CTAs, all of them in flight in one CTA (8 queries of 1,000 keys 9.9 us against 11.8 by
     // a pair, one of 132 keys 8.4 against 9.6 by two CTAs).  Else a pair, whose two warpgroups share three tiles in flight,
     // where a CTA has one item or long ones (148 queries of 640 keys 19.6 us against 24.6 by two CTAs, 300 of 4,096 150
@@ -1172,11 +1173,10 @@ cudaError_t launch_pages_attn(const PagesAttnParams& p, int64_t keys, void* ws, 
         e = pool_map(p.prefix, unit, &mp);
         if (e != cudaSuccess) return e;
     }
-    e = pl.nq == 4   ? launch<4, 2, false, 1>(a, mo, mp, st)
-        : pl.nq == 2 ? launch<2, 1, false, 2>(a, mo, mp, st)
-        : pl.pair    ? launch<1, 3, true, 1, true>(a, mo, mp, st)
-        : pl.two     ? launch<1, 1, true, 2>(a, mo, mp, st)
-                     : launch<1, 3, true, 1>(a, mo, mp, st);
+    e = pl.nq == 4 ? launch<4, 2, false, 1>(a, mo, mp, st)
+        : pl.pair  ? launch<1, 3, true, 1, true>(a, mo, mp, st)
+        : pl.two   ? launch<1, 1, true, 2>(a, mo, mp, st)
+                   : launch<1, 3, true, 1>(a, mo, mp, st);
     if (e != cudaSuccess || pl.parts == 1) return e;
     a.splits = pl.parts;
     const unsigned rows = (unsigned)(p.B * p.Q * kH);
