@@ -570,10 +570,12 @@ _ws_bytes = {}
 
 
 def _pages_attn_args(op, q, q_pos, pages, keys, out, lse, ws, dev):
-    """Outputs and addresses of a paged attention call: (out, lse, Q, q, q_pos, out, lse, ws, its bytes).
+    """Outputs, workspace and addresses of a paged attention call: (out, lse, ws, Q, q, q_pos, out, lse, ws, its bytes).
 
     Without a caller's workspace the call gets one of its own: torch's allocator orders its reuse by
-    stream, and a captured call keeps its in the graph's pool.  A call whose keys are not split needs none."""
+    stream, and a captured call keeps its in the graph's pool.  The caller holds the tensor until the
+    library has returned: its launches are made without the interpreter's lock, and a block given back
+    before the last of them could become another thread's.  A call whose keys are not split needs none."""
     shape = q_pos.shape
     if len(shape) != 2 or shape[0] != pages.B:
         raise ValueError(f"q_pos: expected [{pages.B}, Q], got {tuple(shape)}")
@@ -596,14 +598,15 @@ def _pages_attn_args(op, q, q_pos, pages, keys, out, lse, ws, dev):
     if ws is not None:
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"ws: expected a contiguous tensor on cuda:{dev}, got one on {ws.device}")
-        return out, lse, Q, qp, pp, op_, lp, ws.data_ptr(), ws.numel() * ws.element_size()
+        return out, lse, ws, Q, qp, pp, op_, lp, ws.data_ptr(), ws.numel() * ws.element_size()
     key = (op, B, Q, keys)
     nbytes = _ws_bytes.get(key)
     if nbytes is None:
         nbytes = _ws_bytes[key] = lib().csa2_workspace_bytes(op, B, Q, keys, 0, 0)
     if nbytes <= 256:   # nothing is split: the call does not touch it
-        return out, lse, Q, qp, pp, op_, lp, _flag(dev), nbytes
-    return out, lse, Q, qp, pp, op_, lp, q.new_empty_strided((nbytes,), (1,), dtype=torch.uint8).data_ptr(), nbytes
+        return out, lse, None, Q, qp, pp, op_, lp, _flag(dev), nbytes
+    ws = q.new_empty_strided((nbytes,), (1,), dtype=torch.uint8)
+    return out, lse, ws, Q, qp, pp, op_, lp, ws.data_ptr(), nbytes
 
 
 def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None, sm_scale=1.0 / math.sqrt(D),
@@ -614,8 +617,8 @@ def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None
         raise ValueError(f"window and n_sink are 32-bit numbers, got {window} and {n_sink}")
     dev = torch.cuda.current_device()
     pg, flag = pages.c(dev), _flag(dev)
-    out, lse, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_WINDOW_ATTN, q, q_pos, pages, min(window + n_sink, pages.cap),
-                                                           out, lse, ws, dev)
+    out, lse, ws, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_WINDOW_ATTN, q, q_pos, pages,
+                                                               min(window + n_sink, pages.cap), out, lse, ws, dev)
     rp = None if replay_start is None else _on(replay_start, torch.int32, pages.B, "replay_start", dev)
     st = lib().csa2_window_attn(qp, pg, pp, Q, window, n_sink, rp, sm_scale, op, lp, wp, wn, flag, _raw_stream(dev))
     if st:
@@ -628,8 +631,8 @@ def csa2_prefix_attn(q, prefix, pages, q_pos, sm_scale=1.0 / math.sqrt(D), out=N
     under one causal softmax.  q bf16 [B,Q,16,512], q_pos i32 [B,Q] -> out bf16 (, lse f32 [B,Q,16])."""
     dev = torch.cuda.current_device()
     pf, pg, flag = prefix.c(dev), pages.c(dev), _flag(dev)
-    out, lse, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_PREFIX_ATTN, q, q_pos, pages, prefix.cap + pages.cap, out, lse,
-                                                           ws, dev)
+    out, lse, ws, Q, qp, pp, op, lp, wp, wn = _pages_attn_args(OP_PREFIX_ATTN, q, q_pos, pages, prefix.cap + pages.cap,
+                                                               out, lse, ws, dev)
     st = lib().csa2_prefix_attn(qp, pf, pg, pp, Q, sm_scale, op, lp, wp, wn, flag, _raw_stream(dev))
     if st:
         _check(st)
