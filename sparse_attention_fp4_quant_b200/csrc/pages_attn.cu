@@ -1125,9 +1125,16 @@ cudaError_t pool_map(const csa2_pages& pg, int unit, CUtensorMap* map) {
     const cuuint64_t rows = (cuuint64_t)(pg.n_pages * pg.page_size);
     const cuuint64_t dims[4] = {128, kGroup, kBlocks, rows / kGroup}, strides[3] = {kD, 128, (cuuint64_t)kGroup * kD};
     const cuuint32_t es[4] = {1, 1, 1, 1}, box[4] = {128, kGroup, kBlocks, (cuuint32_t)(unit / kGroup)};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    const auto encode = [&] {
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pg.kv, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (encode() == CUDA_SUCCESS) return cudaSuccess;
+    // The encoder is the driver's and needs a context.  A host thread has none before its first call of the runtime that
+    // works on the device, and in such a thread this is the first: bind the current device's.
+    const cudaError_t e = cudaSetDevice(current_device());
+    if (e != cudaSuccess) return e;
+    return encode() == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int NQ, int ST, bool kConcat, int kCtas, bool kPair = false>
