@@ -10,6 +10,7 @@ raised.
 import ctypes
 import math
 import os
+import threading
 
 import torch
 
@@ -524,7 +525,7 @@ class Pages:
         return self._c
 
 
-_flags = {}
+_flags, _flags_lock = {}, threading.Lock()
 
 
 def _flag(dev):
@@ -532,11 +533,14 @@ def _flag(dev):
     process, so that captured graphs can name it)."""
     f = _flags.get(dev)
     if f is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("make one paged attention call on this device before capturing one into a graph")
-        t = torch.zeros(64, dtype=torch.int32, device=f"cuda:{dev}")
-        torch.cuda.current_stream().synchronize()   # other streams may use it next
-        f = _flags[dev] = (t.data_ptr(), t)
+        with _flags_lock:   # threads whose first calls come together take one flag
+            f = _flags.get(dev)
+            if f is None:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("make one paged attention call on this device before capturing one into a graph")
+                t = torch.zeros(64, dtype=torch.int32, device=f"cuda:{dev}")
+                torch.cuda.current_stream().synchronize()   # other streams may use it next
+                f = _flags[dev] = (t.data_ptr(), t)
     return f[0]
 
 

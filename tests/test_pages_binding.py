@@ -1,4 +1,6 @@
 """The Python binding of the paged cache, on the host alone: a stand-in for the library looks at what it is handed."""
+import threading
+import time
 import weakref
 
 import pytest
@@ -65,3 +67,32 @@ def test_workspace_is_held_during_the_call(host, call, lse):
         csa.csa2_prefix_attn(q, prefix, pages, q_pos, lse=lse)
     assert host.held == [[True]]
     assert [ref() for dtype, ptr, ref in Rows.made if dtype == torch.uint8] == [None]   # and by nobody after it
+
+
+def test_one_flag_for_all_threads(monkeypatch):
+    """Threads whose first calls come together share one flag, which stays: the kernels keep its address."""
+    made = []
+
+    def zeros(*args, **kw):
+        made.append(torch.ones(64, dtype=torch.int32))
+        time.sleep(0.05)   # the other threads come past meanwhile
+        return made[-1]
+
+    class Stream:
+        def synchronize(self):
+            pass
+    monkeypatch.setattr(csa, "_flags", {})
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    got, start = [], threading.Barrier(4)
+
+    def work():
+        start.wait()
+        got.append(csa._flag(0))
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(made) == 1 and got == [made[0].data_ptr()] * 4 and csa._flag(0) == got[0]
