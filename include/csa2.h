@@ -312,7 +312,8 @@ typedef enum {
     CSA2_OP_SPARSE_ATTN = 3,
     CSA2_OP_LAYER = 4,
     CSA2_OP_WINDOW_ATTN = 5,   /* cap = most keys a query sees: min(window + n_sink, max_pages page_size); k, P unused */
-    CSA2_OP_PREFIX_ATTN = 6    /* cap = max_pages page_size of the prefix plus that of the own pages; k, P unused */
+    CSA2_OP_PREFIX_ATTN = 6    /* cap = max_pages page_size of the prefix plus that of the own pages; k, P unused.  Both
+                                  return 0 for more queries (B Q) than a call takes, 65,535 */
 } csa2_op;
 CSA2_API size_t csa2_workspace_bytes(csa2_op op, int32_t B, int32_t Q, int64_t cap, int32_t k, int32_t P);
 

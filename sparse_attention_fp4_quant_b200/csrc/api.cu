@@ -49,10 +49,13 @@ SelectParams select_params(const csa2_kv* kv, const int32_t* q_pos, int B, int Q
     return p;
 }
 
+// Limits of the paged cache: positions and pool rows below 2^31; queries of an attention call.
+constexpr int64_t kPagesMaxTokens = int64_t(1) << 31, kPagesMaxQueries = 65535;
+
 bool pages_ok(const csa2_pages* p) {
     if (!p || !p->kv || !p->kv_sc || !p->table || !p->n_tokens || !aligned16(p->kv) || !aligned16(p->kv_sc)) return false;
     if (p->page_size < 8 || p->page_size > 4096 || p->page_size % 8 != 0) return false;
-    const int64_t lim = int64_t(1) << 31;
+    const int64_t lim = kPagesMaxTokens;
     if (p->B < 1 || p->max_pages < 1 || p->pos0 < 0 || p->n_pages < 1) return false;
     return p->n_pages < lim / p->page_size && (int64_t)p->max_pages * p->page_size + p->pos0 < lim;
 }
@@ -63,7 +66,7 @@ bool pages_attn_ok(const void* q, const csa2_pages* pages, const int32_t* q_pos,
     if (!pages_ok(pages) || !q || !q_pos || !out || !ws || !aligned16(q) || !aligned16(out) || !aligned16(ws))
         return false;
     if (!(sm_scale > 0.0f) || !(sm_scale < 1e30f)) return false;
-    return Q >= 1 && (int64_t)pages->B * Q <= 65535;
+    return Q >= 1 && (int64_t)pages->B * Q <= kPagesMaxQueries;
 }
 
 int64_t pages_cap(const csa2_pages* p) { return (int64_t)p->max_pages * p->page_size; }
@@ -158,8 +161,11 @@ size_t csa2_workspace_bytes(csa2_op op, int32_t B, int32_t Q, int64_t cap, int32
             if (d > m) m = d;
             return m;
         }
-        case CSA2_OP_WINDOW_ATTN: return pages_attn_ws_bytes(false, B, Q, cap);
-        case CSA2_OP_PREFIX_ATTN: return pages_attn_ws_bytes(true, B, Q, cap);
+        case CSA2_OP_WINDOW_ATTN:
+        case CSA2_OP_PREFIX_ATTN:
+            if ((int64_t)B * Q > kPagesMaxQueries) return 0;
+            if (cap > 2 * kPagesMaxTokens) cap = 2 * kPagesMaxTokens;   // the prefix and the own pages
+            return pages_attn_ws_bytes(op == CSA2_OP_PREFIX_ATTN, B, Q, cap);
     }
     return 0;
 }

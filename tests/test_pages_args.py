@@ -104,3 +104,15 @@ def test_window_beyond_32_bits_is_refused(csa, window, n_sink):
     """Not cut down to some other window."""
     with pytest.raises(ValueError, match="32-bit"):
         csa.csa2_window_attn(None, None, None, window=window, n_sink=n_sink)
+
+
+def test_workspace_of_sizes_that_no_call_takes(csa):
+    """Block counts beyond 32 bits end in a size of zero, tables beyond any in the largest one's."""
+    L = csa.lib()
+    for op in (csa.OP_WINDOW_ATTN, csa.OP_PREFIX_ATTN):
+        for B, Q in ((1 << 18, 1 << 16), (65536, 65536), (2 ** 31 - 1, 2 ** 31 - 1), (1, 65536), (65536, 1), (256, 256)):
+            assert L.csa2_workspace_bytes(op, B, Q, 1000, 0, 0) == 0
+        for B, Q in ((1, 1), (4, 1), (1, 65535), (65535, 1), (21, 2)):
+            assert L.csa2_workspace_bytes(op, B, Q, -5, 0, 0) == L.csa2_workspace_bytes(op, B, Q, 0, 0, 0) >= 256
+            top = L.csa2_workspace_bytes(op, B, Q, 1 << 32, 0, 0)
+            assert L.csa2_workspace_bytes(op, B, Q, 2 ** 63 - 1, 0, 0) == top >= 256
