@@ -442,8 +442,9 @@ CSA2_API csa2_status csa2_index_topk_noalloc_status(int32_t clear, void* stream)
  *             table[b][(p - pos0) / page_size], for pos0 <= p < pos0 + n_tokens[b]
  *   page_size a multiple of 8, 8..4096;  n_pages page_size and pos0 + max_pages page_size below 2^31
  *   pos0      token position of the tables' first slot (0, or the length of a shared prefix)
- * Slots of no visible token may hold any bytes.  E4M3 NaN bytes and negative,
- * infinite or NaN scales in a slot that a query of the call sees are not valid input.
+ * Slots of no visible token may hold any bytes.  A NaN byte or scale of a token
+ * makes NaN of the results of every query that sees it, and changes no other query's.
+ * Negative and infinite scales in a slot that a query of the call sees are not valid input.
  */
 typedef struct csa2_pages {
     uint8_t* kv;

@@ -18,8 +18,9 @@
 // reference is the maximum of z + log2(token scale), the size of what enters P, and it moves
 // only when a tile exceeds it by 2^3 (P keeps that much room), so the accumulators are
 // rescaled rarely.  l = sum 2^(z - m) stays in fp32 registers.
-// A slot that no query sees may hold NaN bytes, and a weight of 0 times NaN is NaN.  Such a key's
-// S is NaN as well, so its thread finds out for nothing, and zeroes the row before P K.
+// A slot may hold NaN bytes, and a weight of 0 times NaN is NaN: a query that does not see the key would
+// get it.  Such a key's S is NaN in every column, so its threads find out for nothing, and zero the row
+// before P K.  A query that does see it has a NaN weight there, and gets NaN by that.
 //
 // What bounds it (B200, calls in a graph; the join included):
 //   many queries over long lists  64 rows x 128 keys are 16 products of 64 cycles for S and 48 of 48 cycles for O, 3,340
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                     auto sums = [&](uint32_t (&u)[32]) {   // hi in u[0 .. 15], lo in u[16 .. 31]
                         tmem_ld_32x32b_x32(tq + kS0 + (n & 1) * 2 * RQ + 32 * query, u);
                         tmem_ld_wait();
-                        dirty = !seen && isnan(__uint_as_float(u[0]));
+                        dirty = isnan(__uint_as_float(u[0]));   // in every query of the tile alike, or they would not share the zeroing
                     };
                     const bool first = i < kTurn;
                     bool move = first;
@@ -938,7 +939,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                     ok = wait(&sm.pv_done[0], ppar(n - 1)) && ok;
                 }
                 if (!active && lane == 0 && ok) mbar_arrive(&sm.s_free[n & 1]);
-                if (dirty && ok) {   // S of this tile is done: only P K still reads the row
+                if (dirty && ok) {   // S of this tile is done: only P K still reads the row, of which each query zeroes a part
                     for (int b = query - tile.qa; b < kBlocks; b += tile.nq)
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
