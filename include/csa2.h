@@ -462,7 +462,7 @@ typedef struct csa2_pages {
  *   for k = 0..31, (a, b) = (n_{448+2k}, n_{449+2k}):
  *       a' = a cos t - b sin t,  b' = a sin t + b cos t,  t = pos[r] * inv_freq[k]
  *       (the product in fp64, so that far positions keep their angle)
- *   scale = amax|n| / 448;  code = E4M3 nearest (ties to even) to n / scale, 0 for a zero row
+ *   scale = amax|n| / 448;  code = E4M3 nearest (ties to even) to n / scale; both 0 for a zero row
  * and writes code and scale to the slot of position pos[r] of sequence seq[r].
  *   x         device bf16, row r at x + r * x_stride elements; 16-byte aligned, x_stride a
  *             multiple of 8, >= 512

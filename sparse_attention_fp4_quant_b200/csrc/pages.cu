@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(32 * kPW, kPCtas) pages_append_kernel(const ui
                         make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
             }
             *reinterpret_cast<uint16_t*>(dst + 448 + 2 * lane) = (uint16_t)e4m3x4(v[16] * inv, v[17] * inv, 0.0f, 0.0f);
-            if (lane == 0) pg.kv_sc[row] = a448 * rn * down;
+            if (lane == 0) pg.kv_sc[row] = mx > 0.0f ? a448 * rn * down : 0.0f;   // without an epsilon a zero row's rn is infinite
         }
         if (!more) break;
         r += step;

@@ -673,3 +673,31 @@ def test_timeout_of_long_lists(csa):
         csa.lib().csa2_test_starve_copies(0)
     csa.csa2_flag_status()
     check(*run_window(csa, cache, q, q_pos, 2200, 4), reference(q, q_pos, [(cache, True)], 2200, 4))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-6])
+@pytest.mark.parametrize("rope", [False, True])
+def test_append_zero_rows(csa, eps, rope):
+    """A zero row is stored as zeros of scale 0, without an epsilon too, and reads as a token of logit 0."""
+    rows = 37
+    x = torch.randn((rows, D), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    x[::4] = 0
+    cache = Cache(82, [rows], 8)
+    cache.kv_sc[:] = -7.0
+    pages = cache.gpu()
+    w, f = (torch.arange(D) / D + 0.5).cuda(), inv_freq_table() if rope else None
+    pos = torch.arange(rows, dtype=torch.int32).cuda()
+    csa.csa2_pages_append(x.cuda(), pages, torch.zeros_like(pos), pos, inv_freq=f, norm_w=w, eps=eps)
+    kv, sc = pages.kv.cpu().numpy(), pages.kv_sc.cpu().numpy()
+    live = np.arange(rows) % 4 != 0
+    y, scale = append_reference(x[live], np.arange(rows)[live], f, w, eps, True)
+    for r in range(0, rows, 4):
+        assert not E4M3[kv[cache.row(0, r)]].any() and sc[cache.row(0, r)] == 0
+    for r, yr, s in zip(np.flatnonzero(live), y, scale):
+        at = cache.row(0, int(r))
+        assert abs(sc[at] - s) <= 2.0 ** -18 * s
+        assert (np.abs(E4M3[kv[at]] - yr / s) <= 2.0 ** -4 * np.abs(yr / s) + 2.0 ** -10 + 448 * 2.0 ** -18).all()
+    now = Cache(0, [rows], 8)
+    now.kv, now.kv_sc, now.table = kv, sc, cache.table
+    q, q_pos = queries(4, 1, 1), np.array([[rows - 1]], np.int32)
+    check(*run_window(csa, pages, q, q_pos, 1 << 30, 0), reference(q, q_pos, [(now, True)], 1 << 30, 0))
