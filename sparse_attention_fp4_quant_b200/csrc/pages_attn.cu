@@ -292,7 +292,6 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ul = args.unit_log2, unit = 1 << ul, upt = kTileKeys >> ul;   // keys of a unit, units of a tile
 
-    if (warp == kIssuer) tmem_alloc(&sm.tmem, kTmemCols);
     if (tid == 32 * kProducer) {
         for (int s = 0; s < ST; ++s)
             for (int c = 0; c < kParts; ++c) {
@@ -313,11 +312,18 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         sm.dead = 0;
     }
     if (tid < R) sm.mref[tid] = -INFINITY;
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sm.tmem;
     pdl_enter();
+    // TMEM is taken behind the wait.  Held through it, the columns could be those that a CTA of the kernel before waits for
+    // on this SM, without a limit: the kernels let the next one start before they allocate.
+    if (warp == kIssuer) tmem_alloc(&sm.tmem, kTmemCols);
+    // Its address, for all but the producer, which goes ahead meanwhile.
+    auto tmem_base = [&]() -> uint32_t {
+        tc_fence_before();
+        asm volatile("bar.sync %0, %1;" ::"n"(1 + W), "n"(kWg * W + 64) : "memory");
+        tc_fence_after();
+        return sm.tmem;
+    };
 
     // A bounded wait; the first to run out of time tells every other.  From then on producer and issuers stop, and softmax
     // threads pass their waits but arrive for nothing any more: a stage that never filled must not be freed and armed
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         // ---- S issuer.  S and O have a warp each: one thread issues a product in about 50 cycles, more than most of
         // these take, and each stream's waits then leave the other alone.  A tile's products are unrolled.
         const uint32_t lead = elect_one();
-        const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem_base(), 0);
         const uint32_t k0 = smem_u32(sm.K[0]);
         const uint64_t qd = smem_desc(smem_u32(sm.Qs), 16, 1024, kSw128);
         bool ok = true;
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     } else if (warp == kIssuer + 1) {
         // ---- O issuer ----
         const uint32_t lead = elect_one();
-        const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t td = __shfl_sync(0xFFFFFFFFu, tmem_base(), 0);
         const uint32_t k0 = smem_u32(sm.K[0]);
         const uint64_t pd = smem_desc(smem_u32(sm.P), 128, 2048, kLayoutNone);
         bool ok = true;
@@ -634,7 +640,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
     } else {
         // ---- softmax: warpgroup = query (or every other tile of one), thread = key ----
         const int wg = warp >> 2, query = kPair ? 0 : wg, key = tid & (kWg - 1), quarter = warp & 3;
-        const uint32_t tq = tmem + ((uint32_t)(quarter * 32) << 16);
+        uint32_t tq = 0;   // this warp's lanes of TMEM
         // this warpgroup's accumulator columns: 16 of each channel block (and of each term)
         auto ocol = [&](int b, int x) -> uint32_t { return tq + wg * kOSet + b * kOCols + x * RQ + kH * query; };
         constexpr int kTerms = kConcat ? 3 : 1;
@@ -670,6 +676,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
                         v[k][1] = __ldg(src + 1);
                     }
                 }
+                if (k_item == 0) tq = tmem_base() + ((uint32_t)(quarter * 32) << 16);   // no CTA is without an item
                 bool told = wait(&sm.item_full[k_item & 1], (uint32_t)((k_item >> 1) & 1));
                 // the other warpgroup's last S of the item before still reads Q
                 if (kPair && n > 0) told = wait(&sm.s_full[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1)) && told;
@@ -974,7 +981,7 @@ __global__ void __launch_bounds__(kWg * (kPair ? 2 : NQ) + kAux, kCtas)
         }
     }
     __syncthreads();
-    if (warp == kIssuer) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kIssuer) tmem_dealloc(sm.tmem, kTmemCols);
 }
 
 // Joins the splits of a block, weight 2^(m_s - M) / L with L = sum_s l_s 2^(m_s - M).  The weights come first, a thread
