@@ -484,11 +484,16 @@ CSA2_API csa2_status csa2_pages_append(const void* x, int64_t x_stride, int64_t 
  *   { j <= i : j > i - window and j >= replay_start[b] }  and  { j <= i : j < n_sink },
  * one softmax for each head: z_j = (q_h . k_j) * sm_scale, out_h = sum_j softmax(z)_j k_j.
  *   q, out, lse   as for csa2_sparse_attn; a query that sees no token gets zeros and -inf
- *   q_pos         device int32 [B][Q], any order, negative = no query (a shorter sequence)
+ *   q_pos         device int32 [B][Q], B Q <= 65,535 (a longer chunk is given in parts); any order, negative = no
+ *                 query (a shorter sequence).  Up to four queries that follow one another share the tokens from the
+ *                 first that one of them sees to the last: far-apart positions are right, but slow
  *   window        >= 1 (2^31 - 1: causal attention over everything stored);  n_sink >= 0
  *   replay_start  device int32 [B] or NULL
  *   ws, ws_bytes  device workspace of csa2_workspace_bytes(CSA2_OP_WINDOW_ATTN, ...), 16-byte aligned;
  *                 its contents do not matter.  Calls that may run at the same time need their own.
+ *                 The size is that of these very B, Q and cap, and smaller calls can need more, as they split
+ *                 their keys further.  One buffer for calls of any shape: 256 bytes and the larger of 19,474,432
+ *                 and 65,792 B Q, with the largest B Q, are enough.
  *   Numerics: fp32 logits, softmax statistics and sums; the query is held to 2^-17 of a head's
  *                 largest element, a weight times its token's scale to 2^-9 of itself, or 2^-29 of the
  *                 row's largest where that is more.

@@ -116,3 +116,19 @@ def test_workspace_of_sizes_that_no_call_takes(csa):
             assert L.csa2_workspace_bytes(op, B, Q, -5, 0, 0) == L.csa2_workspace_bytes(op, B, Q, 0, 0, 0) >= 256
             top = L.csa2_workspace_bytes(op, B, Q, 1 << 32, 0, 0)
             assert L.csa2_workspace_bytes(op, B, Q, 2 ** 63 - 1, 0, 0) == top >= 256
+
+
+def test_workspace_of_calls_of_any_shape(csa):
+    """The bound that the header gives for a buffer that serves every shape; sizes are not monotone in any argument."""
+    L, larger = csa.lib(), 0
+    for op in (csa.OP_WINDOW_ATTN, csa.OP_PREFIX_ATTN):
+        for B in (*range(1, 40), 61, 74, 75, 148, 149, 296, 297, 512, 4096, 65535):
+            for Q in (*range(1, 12), 16, 128, 1017, 4096, 65535):
+                if B * Q > 65535:
+                    continue
+                sizes = [L.csa2_workspace_bytes(op, B, Q, n, 0, 0) for n in (1, 132, 384, 385, 600, 2048, 5000, 131072, 1 << 32)]
+                assert 256 <= min(sizes) and max(sizes) <= 256 + max(19474432, 65792 * B * Q)
+                larger = max(larger, *sizes)
+    assert larger == 256 + 65792 * 65535
+    assert L.csa2_workspace_bytes(csa.OP_WINDOW_ATTN, 1, 4096, 1028, 0, 0) == 256
+    assert L.csa2_workspace_bytes(csa.OP_WINDOW_ATTN, 1, 1, 1028, 0, 0) > 256
