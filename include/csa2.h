@@ -458,7 +458,8 @@ typedef struct csa2_pages {
 /*
  * Append to the paged cache: RMSNorm, RoPE by the token's own position, and the
  * FP8 row, in one launch.  In fp32 for each row r with 0 <= seq[r] < B:
- *   n = x / sqrt(mean(x^2) + eps) * norm_w   (n = x if normalise == 0)
+ *   n = x / sqrt(mean(x^2) + eps) * norm_w   (n = x * norm_w if normalise == 0; the sum of squares is fp32, so
+ *       |x| below 2^59 is in its range; n is not rounded to bf16 before the codes, as csa2_front_end's row is)
  *   for k = 0..31, (a, b) = (n_{448+2k}, n_{449+2k}):
  *       a' = a cos t - b sin t,  b' = a sin t + b cos t,  t = pos[r] * inv_freq[k]
  *       (the product in fp64, so that far positions keep their angle)
@@ -494,9 +495,10 @@ CSA2_API csa2_status csa2_pages_append(const void* x, int64_t x_stride, int64_t 
  *                 The size is that of these very B, Q and cap, and smaller calls can need more, as they split
  *                 their keys further.  One buffer for calls of any shape: 256 bytes and the larger of 19,474,432
  *                 and 65,792 B Q, with the largest B Q, are enough.
+ *   sm_scale      positive, below 1e30
  *   Numerics: fp32 logits, softmax statistics and sums; the query is held to 2^-17 of a head's
- *                 largest element, a weight times its token's scale to 2^-9 of itself, or 2^-29 of the
- *                 row's largest where that is more.
+ *                 largest element, a weight times its token's scale to 1.25 * 2^-9 of itself (nine bits of
+ *                 an f16), or 2^-29 of the row's largest where that is more (below about 2^-20 of it).
  *   flag          device int32, zero before first use, or NULL: set to 1 when a device-side
  *                 wait ran out of time (2 s); the results of that call are not valid.  Read
  *                 it with csa2_flag_status.  Any number of calls can share it.
@@ -514,7 +516,10 @@ CSA2_API csa2_status csa2_window_attn(const void* q, const csa2_pages* pages, co
  *   prefix  host pointer, prefix->B == 1
  *   pages   host pointer: the sequences' own tokens, usually with pos0 = the prefix's length; a
  *           position that both hold is two tokens, and both are seen
- *   q, q_pos, out, lse, ws, flag: as for csa2_window_attn (CSA2_OP_PREFIX_ATTN)
+ *   q, q_pos, out, lse, ws, flag, sm_scale: as for csa2_window_attn (CSA2_OP_PREFIX_ATTN)
+ * How the keys are split goes by the capacity of the tables (cap), as the host does not know what is stored: tables
+ * much wider than that leave parts without a token, which are joined all the same (4 queries behind 4,096 tokens
+ * 13.1 us with tables of 64 tokens for their own, 17.7 with 32,768).
  */
 CSA2_API csa2_status csa2_prefix_attn(const void* q, const csa2_pages* prefix, const csa2_pages* pages,
                                       const int32_t* q_pos, int32_t Q, float sm_scale, void* out, float* lse, void* ws,

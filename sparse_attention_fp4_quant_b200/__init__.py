@@ -616,7 +616,8 @@ def _pages_attn_args(op, q, q_pos, pages, keys, out, lse, ws, dev):
 def csa2_window_attn(q, pages, q_pos, window=WINDOW, n_sink=0, replay_start=None, sm_scale=1.0 / math.sqrt(D),
                      out=None, lse=False, ws=None):
     """Sliding-window attention over a paged cache; tokens at positions below n_sink stay visible.
-    q bf16 [B,Q,16,512], q_pos i32 [B,Q] (negative = no query) -> out bf16 [B,Q,16,512] (, lse f32 [B,Q,16])."""
+    q bf16 [B,Q,16,512], q_pos i32 [B,Q] (negative = no query) -> out bf16 [B,Q,16,512] (, lse f32 [B,Q,16]).
+    ws: a workspace of the caller's, of csa2_workspace_bytes for this very shape (smaller calls can need more)."""
     if not (-2 ** 31 <= window < 2 ** 31 and -2 ** 31 <= n_sink < 2 ** 31):   # ctypes would cut them off
         raise ValueError(f"window and n_sink are 32-bit numbers, got {window} and {n_sink}")
     dev = torch.cuda.current_device()

@@ -3,9 +3,9 @@
 //
 // A warp takes a row at a time and fetches the next one meanwhile.  Lane l holds channels
 // 8 l .. 8 l + 7, for l < 24 also 256 + 8 l .., and the pair 448 + 2 l, 449 + 2 l: one rotated
-// pair in every lane, each with its own angle.  The kernel is bound by instructions (430 a row
-// in its first form, 20.8 us for 32,768 rows; now 259 and 12.3 us, 4.1 TB/s in and out with the issue
-// slots 67 % busy), and this split takes the fewest.  The angle
+// pair in every lane, each with its own angle.  The time goes with the instructions (430 a row
+// in its first form, 20.8 us for 32,768 rows; now 262 and 12.4 us, 4.1 TB/s in and out with the issue
+// slots 66 % busy), and of the splits tried this takes the fewest.  The angle
 // pos * inv_freq is formed in fp64 and reduced to a fraction of a turn before the fp32 sine: at
 // position 10^6 an fp32 product would be off by up to 0.03 radian.
 // The norm's factor 1 / rms is common to a row, so the codes do not depend on it: it is applied

@@ -12,8 +12,9 @@
 //       elements below 2^-9 of the row's largest (each row scaled by its own power of two),
 //       which are held to 2^-17 of it.  hi and lo are separate columns of S, added in fp32.
 //   P   each weight times its token scale, as f16 with 2^12 of headroom below the maximum,
-//       split in three E5M2 terms (f16's exponent range): at least 9 significant bits; what is
-//       smaller than 2^-26 of the row's largest is held to 2^-29 of it (E5M2's smallest step).
+//       split in three E5M2 terms (f16's exponent range): 9 of the f16's 11 significant bits, so
+//       within 2^-11 + 2^-9 of itself, or 2^-29 of the row's largest where that is more (below
+//       about 2^-20 of it: half of E5M2's smallest step, 2^-16, against 2^12).
 // Softmax: fp32, one thread per key, one pass with a running reference m per row.  The
 // reference is the maximum of z + log2(token scale), the size of what enters P, and it moves
 // only when a tile exceeds it by 2^3 (P keeps that much room), so the accumulators are
@@ -24,14 +25,16 @@
 //
 // What bounds it (B200, calls in a graph; the join included):
 //   many queries over long lists  64 rows x 128 keys are 16 products of 64 cycles for S and 48 of 48 cycles for O, 3,340
-//       of the 5,200 that a tile takes: two tiles fit beside the queries, and a tile's turn (fetch 900 cycles after the
-//       last product of the one before, S 2,200, softmax 2,600, O 3,100, waits) is 10,400 for every second one.  32
-//       queries behind 131,072 tokens 173 us, 0.48 of the time of the products at the measured bf16 rate; 3 x 1,017 of a
-//       1,024-token window 153 us, 0.36.
-//   one query, long lists         the stream: 61 queries of 4,096 tokens in pages of 16 38 us, 5.6 TB/s while it runs.
-//   many queries, short windows   a chain of 19,700 cycles an item (queries in, two tiles, output): 4,096 queries of a
-//       128-token window 77 us.
-//   one token                     the same chain after the launch: 8 us for 1 to 32 sequences.
+//       of the 5,100 that a tile takes: two tiles fit beside the queries, and a tile's turn (fetch 900 cycles after the
+//       last product of the one before, S 2,200, softmax 2,600, O 3,100, waits) is 10,200 for every second one.  32
+//       queries behind 131,072 tokens 174 us, 0.48 of the time of the products at the measured bf16 rate (192 and 0.43
+//       in a long loop of calls, at the power limit's clocks); 3 x 1,017 of a 1,024-token window 149 us, 0.37 (156 and
+//       0.35).
+//   one query, long lists         the stream: 61 queries of 4,096 tokens in pages of 16 37.5 us, 5.6 TB/s while it runs,
+//       by 122 of the 148 SMs.
+//   many queries, short windows   a chain of 17,200 cycles an item (queries in, two tiles, output): 4,096 queries of a
+//       128-token window 75 us.
+//   one token                     the same chain after the launch: 7.6 us for one sequence, 7.9 for 32.
 #include <cuda.h>
 
 #include <algorithm>
